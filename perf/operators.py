@@ -98,7 +98,7 @@ def draw(rng):
     if op == "fp8":
         return {"op": op, "rows": _log(rng, 1, 16384), "experts": rng.randint(1, 48),
                 "n": 16 * rng.randint(16, 256), "k": 128 * rng.randint(2, 40),
-                "out": rng.choice(("bf16", "f16", "f32")), "gated": rng.random() < 0.5,
+                "out": dtype, "gated": rng.random() < 0.5,
                 "align": align, "skew": skew}
     if op == "w4":
         group = rng.choice((32, 64, 128))
