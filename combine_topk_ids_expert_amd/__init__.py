@@ -37,6 +37,8 @@ __all__ = [
     "prepare_moe_input", "shuffle_rows", "dispatch_rows", "apply_shuffle_mul_sum",
     "prepare_dispatch",
     "moe_output_memset", "zero_padding_rows", "moe_sort", "dispatch_rows_fp8",
+    "topk_gating", "topk_gating_backward", "grouped_gemm", "grouped_gemm_fp8", "grouped_gemm_w4",
+    "grouped_gemm_wgrad", "silu_mul_backward",
     "prepare_moe_input_noalloc", "dispatch_capacity", "prepare_workspace_size",
     "empty_routing", "MxError",
     "library_path", "load_library", "open_library", "EXPORTED_SYMBOLS", "bind", "BoundCall",
@@ -76,6 +78,8 @@ EXPORTED_SYMBOLS = (
     "mx_dispatch_rows_timed", "mx_apply_shuffle_mul_sum_timed", "mx_prepare_moe_input_timed",
     "mx_prepare_moe_input_noalloc", "mx_prepare_dispatch",
     "mx_bounds_checked", "mx_bounds_report", "mx_bounds_shrink_outputs",
+    "mx_topk_gating", "mx_topk_gating_backward", "mx_grouped_gemm", "mx_grouped_gemm_fp8",
+    "mx_grouped_gemm_w4", "mx_grouped_gemm_wgrad", "mx_silu_mul_backward",
 )
 
 
@@ -159,6 +163,24 @@ def open_library(path: str):
     lib.mx_moe_sort.restype = ctypes.c_int
     lib.mx_moe_sort.argtypes = [vp, i32, i64, i32, i32, i32, i32, i32, vp, vp, i64, vp, vp, i64,
                                 vp, vp, vp, vp, sz, vp]
+    lib.mx_topk_gating.restype = ctypes.c_int
+    lib.mx_topk_gating.argtypes = [vp, i32, i64, i32, i32, i32, vp, i32, ctypes.c_float, vp, vp, vp]
+    lib.mx_topk_gating_backward.restype = ctypes.c_int
+    lib.mx_topk_gating_backward.argtypes = [vp, i32, i64, i32, i32, i32, i32, ctypes.c_float, vp,
+                                            vp, vp, vp]
+    lib.mx_grouped_gemm.restype = ctypes.c_int
+    lib.mx_grouped_gemm.argtypes = [vp, vp, i32, i64, i32, i64, i64, i32, vp, vp, vp, i32, vp, vp]
+    lib.mx_grouped_gemm_fp8.restype = ctypes.c_int
+    lib.mx_grouped_gemm_fp8.argtypes = [vp, vp, vp, vp, i64, i32, i64, i64, i32, vp, vp, vp, i32,
+                                        vp]
+    lib.mx_grouped_gemm_w4.restype = ctypes.c_int
+    lib.mx_grouped_gemm_w4.argtypes = [vp, i32, vp, vp, vp, i32, i64, i32, i64, i64, i32, vp, vp,
+                                       vp, vp]
+    lib.mx_grouped_gemm_wgrad.restype = ctypes.c_int
+    lib.mx_grouped_gemm_wgrad.argtypes = [vp, vp, i32, i64, i32, i64, i64, vp, vp, vp, i32, i32,
+                                          vp]
+    lib.mx_silu_mul_backward.restype = ctypes.c_int
+    lib.mx_silu_mul_backward.argtypes = [vp, vp, i32, i64, i32, i64, vp, vp, vp, vp]
     lib.mx_bounds_checked.restype = i32
     lib.mx_bounds_checked.argtypes = []
     lib.mx_bounds_report.restype = ctypes.c_int
@@ -291,7 +313,9 @@ def bind(fn, *args, **kwargs) -> BoundCall:
     """Check and marshal ``fn(*args, **kwargs)`` (one of this module's calls)
     once and return a ``BoundCall`` that repeats it without the checks."""
     bindable = (prepare_moe_input, shuffle_rows, dispatch_rows, apply_shuffle_mul_sum,
-                moe_output_memset, zero_padding_rows, dispatch_rows_fp8, prepare_dispatch)
+                moe_output_memset, zero_padding_rows, dispatch_rows_fp8, prepare_dispatch,
+                topk_gating, topk_gating_backward, grouped_gemm, grouped_gemm_fp8,
+                grouped_gemm_w4, grouped_gemm_wgrad, silu_mul_backward)
     if fn not in bindable:
         raise TypeError(f"cannot bind {getattr(fn, '__name__', fn)!r}")
     return fn(*args, _bind=True, **kwargs)
@@ -712,3 +736,273 @@ def dispatch_rows_fp8(input: torch.Tensor, output_permutation: torch.Tensor, top
     return _finish(dev, "mx_dispatch_rows_fp8", args, "dispatch_rows_fp8", _bind, None,
                    (input, output_permutation, output, output_scales))
 
+
+
+# ---- the router ---------------------------------------------------------------
+
+SCORE_SOFTMAX, SCORE_SIGMOID = range(2)
+_SCORING = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+def _gating_args(logits, topk_ids, weights, weights_name, scoring):
+    _check_dev("logits", logits)
+    dev = logits.device
+    if logits.dim() != 2 or logits.dtype not in _FLOAT_CODES:
+        raise TypeError("logits must be a 2-D float32, float16 or bfloat16 tensor")
+    T, E = logits.shape
+    _check_dev("topk_ids", topk_ids, dev)
+    _check_dev(weights_name, weights, dev)
+    _check_i32("topk_ids", topk_ids)
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError("topk_ids must be [tokens, topk]")
+    if weights.dtype != torch.float32 or weights.shape != topk_ids.shape:
+        raise ValueError(f"{weights_name} must be float32 of topk_ids' shape")
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid' (got {scoring!r})")
+    return dev, T, E, topk_ids.shape[1]
+
+
+def topk_gating(logits: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, *,
+                scoring: str = "softmax", bias: torch.Tensor | None = None,
+                renormalize: bool = True, scale: float = 1.0, _bind: bool = False):
+    """The topk experts of every token and their weights from router logits
+    [T, E], in place: topk_ids [T, topk] int32 (largest score first, equal ones
+    by lower index) and topk_weights [T, topk] float32, the softmax over the
+    chosen experts (over all of them without ``renormalize``) or their sigmoids
+    (divided by their sum with it), times ``scale``.  ``bias`` [E] float32 is
+    added to the sigmoids for the selection alone.  Experts with a logit of
+    -inf or NaN are never chosen; places left over hold id -1 and weight 0."""
+    dev, T, E, topk = _gating_args(logits, topk_ids, topk_weights, "topk_weights", scoring)
+    if bias is not None:
+        _check_dev("bias", bias, dev)
+        if bias.dtype != torch.float32 or bias.numel() != E:
+            raise ValueError("bias must be float32 [experts]")
+        if scoring != "sigmoid":
+            raise ValueError("bias goes with sigmoid scoring only")
+    if not T and not _bind:
+        return None
+    args = (_ptr(logits), _FLOAT_CODES[logits.dtype], T, E, topk, _SCORING[scoring], _ptr(bias),
+            int(bool(renormalize)), float(scale), _ptr(topk_ids), _ptr(topk_weights))
+    return _finish(dev, "mx_topk_gating", args, "topk_gating", _bind, None,
+                   (logits, topk_ids, topk_weights, bias))
+
+
+def topk_gating_backward(logits: torch.Tensor, topk_ids: torch.Tensor,
+                         grad_weights: torch.Tensor, grad_logits: torch.Tensor, *,
+                         scoring: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                         _bind: bool = False):
+    """The gradient of topk_gating's logits, in place, from the gradient of its
+    weights: grad_logits has the logits' shape and type, and every element of
+    it is written."""
+    dev, T, E, topk = _gating_args(logits, topk_ids, grad_weights, "grad_weights", scoring)
+    _check_dev("grad_logits", grad_logits, dev)
+    if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
+        raise ValueError("grad_logits must have logits' shape and type")
+    if not T and not _bind:
+        return None
+    args = (_ptr(logits), _FLOAT_CODES[logits.dtype], T, E, topk, _SCORING[scoring],
+            int(bool(renormalize)), float(scale), _ptr(topk_ids), _ptr(grad_weights),
+            _ptr(grad_logits))
+    return _finish(dev, "mx_topk_gating_backward", args, "topk_gating_backward", _bind, None,
+                   (logits, topk_ids, grad_weights, grad_logits))
+
+
+# ---- the experts' products ------------------------------------------------------
+
+GEMM_TRANSPOSED, GEMM_SILU_MUL = 1, 2
+_HALF_CODES = {torch.float16: MX_F16, torch.bfloat16: MX_BF16}
+
+
+def _check_segments(dev, expert_offsets, problem_sizes):
+    """The expert count of a call on expert segments."""
+    _check_dev("expert_offsets", expert_offsets, dev)
+    _check_i32("expert_offsets", expert_offsets)
+    E = expert_offsets.numel() - 1
+    if E < 1:
+        raise ValueError("expert_offsets must have one element more than there are experts")
+    if problem_sizes is not None:
+        _check_dev("problem_sizes", problem_sizes, dev)
+        _check_i32("problem_sizes", problem_sizes, 3 * E)
+    return E
+
+
+def _check_shape(name, t, dev, shape, dtypes):
+    _check_dev(name, t, dev)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]} (got {t.dtype})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+
+
+def _check_half_rows(name, t):
+    _check_dev(name, t)
+    if t.dim() != 2 or t.dtype not in _HALF_CODES:
+        raise TypeError(f"{name} must be a 2-D float16 or bfloat16 tensor")
+
+
+def grouped_gemm(input: torch.Tensor, weight: torch.Tensor, expert_offsets: torch.Tensor,
+                 output: torch.Tensor, problem_sizes: torch.Tensor | None = None, *,
+                 transpose_weight: bool = False, silu_mul: bool = False,
+                 gate_up: torch.Tensor | None = None, _bind: bool = False) -> torch.Tensor:
+    """Every dispatched row times its expert's weights, in place:
+    output[r] = weight[e] @ input[r] for the rows r of segment e (rows from
+    expert_offsets[e] on, problem_sizes[e][0] of them, or all up to
+    expert_offsets[e + 1] without ``problem_sizes``).  Other rows are neither
+    read nor written.
+
+    input [rows, k] and weight [E, n, k] float16 or bfloat16, output [rows, n]
+    float32, float16 or bfloat16.  With ``transpose_weight`` weight is [E, k, n]:
+    the gradient of a product's rows from its output's gradient and its weights
+    as they are.  With ``silu_mul`` weight is [E, 2n, k] (gates, then ups) and
+    output[r] = silu(gate) * up; ``gate_up`` [rows, 2n] then takes both halves
+    for silu_mul_backward."""
+    _check_half_rows("input", input)
+    dev = input.device
+    E = _check_segments(dev, expert_offsets, problem_sizes)
+    R, k = input.shape
+    _check_dev("output", output, dev)
+    if output.dim() != 2:
+        raise ValueError("output must be [rows, n]")
+    n = output.shape[1]
+    if transpose_weight and silu_mul:
+        raise ValueError("transpose_weight and silu_mul exclude each other")
+    _check_shape("weight", weight, dev,
+                 (E, k, n) if transpose_weight else (E, 2 * n if silu_mul else n, k),
+                 (input.dtype,))
+    _check_shape("output", output, dev, (R, n), _FLOAT_CODES)
+    if gate_up is not None:
+        if not silu_mul:
+            raise ValueError("gate_up goes with silu_mul")
+        _check_shape("gate_up", gate_up, dev, (R, 2 * n), (output.dtype,))
+    if not R and not _bind:
+        return output
+    flags = (GEMM_TRANSPOSED if transpose_weight else 0) | (GEMM_SILU_MUL if silu_mul else 0)
+    args = (_ptr(input), _ptr(weight), _HALF_CODES[input.dtype], R, E, n, k, flags,
+            _ptr(expert_offsets), _ptr(problem_sizes), _ptr(output), _FLOAT_CODES[output.dtype],
+            _ptr(gate_up))
+    return _finish(dev, "mx_grouped_gemm", args, "grouped_gemm", _bind, output,
+                   (input, weight, expert_offsets, output, problem_sizes, gate_up))
+
+
+def grouped_gemm_fp8(input: torch.Tensor, input_scales: torch.Tensor, weight: torch.Tensor,
+                     weight_scales: torch.Tensor, expert_offsets: torch.Tensor,
+                     output: torch.Tensor, problem_sizes: torch.Tensor | None = None, *,
+                     silu_mul: bool = False, _bind: bool = False) -> torch.Tensor:
+    """grouped_gemm from FP8 rows and weights, in place: input [rows, k] e4m3fn
+    with input_scales [rows, k / 128] float32 (as dispatch_rows_fp8 writes
+    them), weight [E, n, k] e4m3fn ([E, 2n, k] with ``silu_mul``) with
+    weight_scales [E, ceil(n / 128), k / 128] (of weight's rows), output
+    [rows, n] float16 or bfloat16.  The FP8 tensors may be uint8 views."""
+    _check_dev("input", input)
+    dev = input.device
+    E = _check_segments(dev, expert_offsets, problem_sizes)
+    fp8 = (torch.float8_e4m3fn, torch.uint8)
+    if input.dim() != 2 or input.dtype not in fp8:
+        raise TypeError("input must be a 2-D float8_e4m3fn (or uint8) tensor")
+    R, k = input.shape
+    if k % 128:
+        raise ValueError("k must be a multiple of 128")
+    _check_dev("output", output, dev)
+    if output.dim() != 2:
+        raise ValueError("output must be [rows, n]")
+    n = output.shape[1]
+    wide = 2 * n if silu_mul else n
+    if silu_mul and n % 16:
+        raise ValueError("n must be a multiple of 16 with silu_mul")
+    _check_shape("input_scales", input_scales, dev, (R, k // 128), (torch.float32,))
+    _check_shape("weight", weight, dev, (E, wide, k), fp8)
+    _check_shape("weight_scales", weight_scales, dev, (E, -(-wide // 128), k // 128),
+                 (torch.float32,))
+    _check_shape("output", output, dev, (R, n), _HALF_CODES)
+    if not R and not _bind:
+        return output
+    args = (_ptr(input), _ptr(input_scales), _ptr(weight), _ptr(weight_scales), R, E, n, k,
+            GEMM_SILU_MUL if silu_mul else 0, _ptr(expert_offsets), _ptr(problem_sizes),
+            _ptr(output), _HALF_CODES[output.dtype])
+    return _finish(dev, "mx_grouped_gemm_fp8", args, "grouped_gemm_fp8", _bind, output,
+                   (input, input_scales, weight, weight_scales, expert_offsets, output,
+                    problem_sizes))
+
+
+def grouped_gemm_w4(input: torch.Tensor, weight: torch.Tensor, scales: torch.Tensor,
+                    expert_offsets: torch.Tensor, output: torch.Tensor,
+                    problem_sizes: torch.Tensor | None = None, *,
+                    zeros: torch.Tensor | None = None, silu_mul: bool = False,
+                    _bind: bool = False) -> torch.Tensor:
+    """grouped_gemm with 4-bit weights, for decoding, in place: weight
+    [E, n, k / 2] uint8 ([E, 2n, k / 2] with ``silu_mul``), the lower position in
+    the low four bits of a byte; scales [E, n, k / group] of input's type and
+    ``zeros`` of the same shape, uint8 (8 everywhere without it): a weight is
+    (q - zero) * scale.  group is 32, 64 or 128.  input [rows, k] and output
+    [rows, n] float16 or bfloat16, the same."""
+    _check_half_rows("input", input)
+    dev = input.device
+    E = _check_segments(dev, expert_offsets, problem_sizes)
+    R, k = input.shape
+    _check_dev("output", output, dev)
+    if output.dim() != 2:
+        raise ValueError("output must be [rows, n]")
+    n = output.shape[1]
+    wide = 2 * n if silu_mul else n
+    _check_dev("scales", scales, dev)
+    if scales.dim() != 3 or not scales.shape[2] or k % scales.shape[2] or \
+            k // scales.shape[2] not in (32, 64, 128):
+        raise ValueError("scales must be [E, n, k / group] with groups of 32, 64 or 128")
+    group = k // scales.shape[2]
+    _check_shape("weight", weight, dev, (E, wide, k // 2), (torch.uint8,))
+    _check_shape("scales", scales, dev, (E, wide, k // group), (input.dtype,))
+    if zeros is not None:
+        _check_shape("zeros", zeros, dev, (E, wide, k // group), (torch.uint8,))
+    _check_shape("output", output, dev, (R, n), (input.dtype,))
+    if not R and not _bind:
+        return output
+    args = (_ptr(input), _HALF_CODES[input.dtype], _ptr(weight), _ptr(scales), _ptr(zeros), group,
+            R, E, n, k, GEMM_SILU_MUL if silu_mul else 0, _ptr(expert_offsets),
+            _ptr(problem_sizes), _ptr(output))
+    return _finish(dev, "mx_grouped_gemm_w4", args, "grouped_gemm_w4", _bind, output,
+                   (input, weight, scales, zeros, expert_offsets, output, problem_sizes))
+
+
+def grouped_gemm_wgrad(grad_output: torch.Tensor, input: torch.Tensor,
+                       expert_offsets: torch.Tensor, grad_weight: torch.Tensor,
+                       problem_sizes: torch.Tensor | None = None, *, accumulate: bool = False,
+                       _bind: bool = False) -> torch.Tensor:
+    """The gradient of grouped_gemm's weights, in place: grad_weight[e] =
+    grad_output[segment e].T @ input[segment e], added to what it holds with
+    ``accumulate``; without, an expert without rows gets zeros.  grad_output
+    [rows, n] and input [rows, k] float16 or bfloat16, grad_weight [E, n, k]
+    float32, float16 or bfloat16."""
+    _check_half_rows("grad_output", grad_output)
+    dev = grad_output.device
+    E = _check_segments(dev, expert_offsets, problem_sizes)
+    R, n = grad_output.shape
+    _check_half_rows("input", input)
+    k = input.shape[1]
+    _check_shape("input", input, dev, (R, k), (grad_output.dtype,))
+    _check_shape("grad_weight", grad_weight, dev, (E, n, k), _FLOAT_CODES)
+    args = (_ptr(grad_output), _ptr(input), _HALF_CODES[input.dtype], R, E, n, k,
+            _ptr(expert_offsets), _ptr(problem_sizes), _ptr(grad_weight),
+            _FLOAT_CODES[grad_weight.dtype], int(bool(accumulate)))
+    return _finish(dev, "mx_grouped_gemm_wgrad", args, "grouped_gemm_wgrad", _bind, grad_weight,
+                   (grad_output, input, expert_offsets, grad_weight, problem_sizes))
+
+
+def silu_mul_backward(grad_output: torch.Tensor, gate_up: torch.Tensor,
+                      expert_offsets: torch.Tensor, grad_gate_up: torch.Tensor,
+                      problem_sizes: torch.Tensor | None = None, *,
+                      _bind: bool = False) -> torch.Tensor:
+    """The gradient of grouped_gemm's gated activation on the rows of the
+    segments, in place: grad_gate_up [rows, 2n] from grad_output [rows, n] and
+    the gate_up [rows, 2n] that the product kept.  grad_gate_up may be gate_up."""
+    _check_half_rows("grad_output", grad_output)
+    dev = grad_output.device
+    E = _check_segments(dev, expert_offsets, problem_sizes)
+    R, n = grad_output.shape
+    _check_shape("gate_up", gate_up, dev, (R, 2 * n), (grad_output.dtype,))
+    _check_shape("grad_gate_up", grad_gate_up, dev, (R, 2 * n), (grad_output.dtype,))
+    if not R and not _bind:
+        return grad_gate_up
+    args = (_ptr(grad_output), _ptr(gate_up), _HALF_CODES[gate_up.dtype], R, E, n,
+            _ptr(expert_offsets), _ptr(problem_sizes), _ptr(grad_gate_up))
+    return _finish(dev, "mx_silu_mul_backward", args, "silu_mul_backward", _bind, grad_gate_up,
+                   (grad_output, gate_up, expert_offsets, grad_gate_up, problem_sizes))

@@ -50,6 +50,8 @@ HIPCC_FLAGS = [
     "-ffp-contract=off",
     # Keep the compiler from forming packed fp32 instructions.
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    # Sources side by side.
+    "-parallel-jobs=8",
 ]
 
 

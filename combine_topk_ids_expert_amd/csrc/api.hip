@@ -346,6 +346,42 @@ mx_status prepare_moe_input(const void* topk_ids, int32_t ids_dtype, int64_t num
             rows ? rows->num_dst_rows * rows->side_row_bytes : 0, true});
 }
 
+// ---- expert products ---------------------------------------------------------
+
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;   // columns and contraction of a product
+
+// What every call on expert segments checks: sizes, offsets and row counts.
+mx_status check_segments(int64_t num_rows, int32_t num_experts, int64_t n, int64_t k,
+                         const int32_t* expert_offsets, const int32_t* problem_sizes) {
+    if (num_rows < 0 || num_rows > kMax31 || num_experts < 1 || num_experts > MX_MAX_EXPERTS ||
+        n < 1 || n > kMaxWidth || k < 1 || k > kMaxWidth || expert_offsets == nullptr)
+        return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(expert_offsets, 4) || !aligned(problem_sizes, 4)) return MX_ERR_MISALIGNED;
+    return MX_OK;
+}
+
+mxmoe::GemmArgs product_args(const void* x, const void* w, void* out, int32_t dtype,
+                             int32_t out_dtype, int64_t num_rows, int32_t num_experts, int64_t n,
+                             int64_t k, const int32_t* expert_offsets,
+                             const int32_t* problem_sizes) {
+    mxmoe::GemmArgs a{};
+    a.x = static_cast<const uint8_t*>(x);
+    a.w = static_cast<const uint8_t*>(w);
+    a.out = out;
+    a.offsets = expert_offsets;
+    a.sizes = problem_sizes;
+    a.num_rows = num_rows;
+    a.len = k;
+    a.out_cols = n;
+    a.num_experts = num_experts;
+    a.dtype = dtype;
+    a.out_dtype = out_dtype;
+    a.vector_store = n % 4 == 0 && aligned(out, 4 * (size_t)elem_bytes(out_dtype));
+    return a;
+}
+
+bool rows16(const void* p, int64_t row_bytes) { return aligned(p, 16) && row_bytes % 16 == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -676,6 +712,238 @@ mx_status mx_dispatch_rows_fp8(const void* src, int32_t src_dtype, int64_t num_t
                       Buf{output_permutation, num_tokens * topk * 4, false},
                       Buf{dst_q, num_dst_rows * hidden, true},
                       Buf{dst_scales, num_dst_rows * (hidden / 128) * 4, true});
+}
+
+mx_status mx_grouped_gemm(const void* x, const void* w, int32_t dtype, int64_t num_rows,
+                          int32_t num_experts, int64_t n, int64_t k, int32_t flags,
+                          const int32_t* expert_offsets, const int32_t* problem_sizes, void* out,
+                          int32_t out_dtype, void* gate_up, void* stream) {
+    if (dtype != MX_F16 && dtype != MX_BF16) return MX_ERR_UNSUPPORTED_DTYPE;
+    const int64_t ob = elem_bytes(out_dtype);
+    if (ob == 0) return MX_ERR_UNSUPPORTED_DTYPE;
+    const mx_status st = check_segments(num_rows, num_experts, n, k, expert_offsets, problem_sizes);
+    if (st != MX_OK) return st;
+    const bool gated = flags & MX_GEMM_SILU_MUL, transposed = flags & MX_GEMM_TRANSPOSED;
+    if ((flags & ~(MX_GEMM_SILU_MUL | MX_GEMM_TRANSPOSED)) != 0 || (gated && transposed) ||
+        (!gated && gate_up != nullptr))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (num_rows > 0 && (x == nullptr || w == nullptr || out == nullptr))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 2) || !aligned(w, 2) || !aligned(out, (size_t)ob) ||
+        !aligned(gate_up, (size_t)ob))
+        return MX_ERR_MISALIGNED;
+    if (num_rows == 0) return MX_OK;
+    mxmoe::GemmArgs a = product_args(x, w, out, dtype, out_dtype, num_rows, num_experts, n, k,
+                                     expert_offsets, problem_sizes);
+    const int64_t w_rows = transposed ? k : gated ? 2 * n : n;
+    a.gate_up = gate_up;
+    a.gated = gated;
+    a.transposed = transposed;
+    a.x_row_bytes = k * 2;
+    a.w_row_bytes = (transposed ? n : k) * 2;
+    a.w_expert_bytes = w_rows * a.w_row_bytes;
+    a.aligned = rows16(x, a.x_row_bytes) && rows16(w, a.w_row_bytes);
+    a.vector_store = a.vector_store && aligned(gate_up, 4 * (size_t)ob);
+    return MX_BOUNDED(stream,
+                      hip_status(mxmoe::launch_grouped_gemm(a, static_cast<hipStream_t>(stream))),
+                      Buf{x, num_rows * a.x_row_bytes, false},
+                      Buf{w, num_experts * a.w_expert_bytes, false},
+                      Buf{expert_offsets, ((int64_t)num_experts + 1) * 4, false},
+                      Buf{problem_sizes, (int64_t)num_experts * 12, false},
+                      Buf{out, num_rows * n * ob, true},
+                      Buf{gate_up, num_rows * 2 * n * ob, true});
+}
+
+mx_status mx_grouped_gemm_fp8(const void* x, const float* x_scales, const void* w,
+                              const float* w_scales, int64_t num_rows, int32_t num_experts,
+                              int64_t n, int64_t k, int32_t flags, const int32_t* expert_offsets,
+                              const int32_t* problem_sizes, void* out, int32_t out_dtype,
+                              void* stream) {
+    if (out_dtype != MX_F16 && out_dtype != MX_BF16) return MX_ERR_UNSUPPORTED_DTYPE;
+    const mx_status st = check_segments(num_rows, num_experts, n, k, expert_offsets, problem_sizes);
+    if (st != MX_OK) return st;
+    const bool gated = flags & MX_GEMM_SILU_MUL;
+    if ((flags & ~MX_GEMM_SILU_MUL) != 0 || k % 128 != 0 || (gated && n % 16 != 0))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (num_rows > 0 && (x == nullptr || x_scales == nullptr || w == nullptr ||
+                         w_scales == nullptr || out == nullptr))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
+        !aligned(out, 2))
+        return MX_ERR_MISALIGNED;
+    if (num_rows == 0) return MX_OK;
+    mxmoe::GemmArgs a = product_args(x, w, out, MX_FP8_E4M3, out_dtype, num_rows, num_experts, n,
+                                     k, expert_offsets, problem_sizes);
+    const int64_t w_rows = gated ? 2 * n : n;
+    a.gated = gated;
+    a.x_scales = x_scales;
+    a.w_scales = w_scales;
+    a.w_scale_rows = (int32_t)((w_rows + 127) / 128);
+    a.x_row_bytes = a.w_row_bytes = k;
+    a.w_expert_bytes = w_rows * k;
+    a.aligned = true;
+    return MX_BOUNDED(stream,
+                      hip_status(mxmoe::launch_grouped_gemm(a, static_cast<hipStream_t>(stream))),
+                      Buf{x, num_rows * k, false},
+                      Buf{x_scales, num_rows * (k / 128) * 4, false},
+                      Buf{w, num_experts * a.w_expert_bytes, false},
+                      Buf{w_scales, (int64_t)num_experts * a.w_scale_rows * (k / 128) * 4, false},
+                      Buf{expert_offsets, ((int64_t)num_experts + 1) * 4, false},
+                      Buf{problem_sizes, (int64_t)num_experts * 12, false},
+                      Buf{out, num_rows * n * 2, true});
+}
+
+mx_status mx_grouped_gemm_w4(const void* x, int32_t dtype, const void* w, const void* scales,
+                             const uint8_t* zeros, int32_t group, int64_t num_rows,
+                             int32_t num_experts, int64_t n, int64_t k, int32_t flags,
+                             const int32_t* expert_offsets, const int32_t* problem_sizes,
+                             void* out, void* stream) {
+    if (dtype != MX_F16 && dtype != MX_BF16) return MX_ERR_UNSUPPORTED_DTYPE;
+    const mx_status st = check_segments(num_rows, num_experts, n, k, expert_offsets, problem_sizes);
+    if (st != MX_OK) return st;
+    const bool gated = flags & MX_GEMM_SILU_MUL;
+    if ((flags & ~MX_GEMM_SILU_MUL) != 0 || (group != 32 && group != 64 && group != 128) ||
+        k % group != 0)
+        return MX_ERR_INVALID_ARGUMENT;
+    if (num_rows > 0 && (x == nullptr || w == nullptr || scales == nullptr || out == nullptr))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(scales, 2) || !aligned(out, 2))
+        return MX_ERR_MISALIGNED;
+    if (num_rows == 0) return MX_OK;
+    mxmoe::GemmArgs a = product_args(x, w, out, dtype, dtype, num_rows, num_experts, n, k,
+                                     expert_offsets, problem_sizes);
+    const int64_t w_rows = gated ? 2 * n : n;
+    [[maybe_unused]] const int64_t num_scales = num_experts * w_rows * (k / group);
+    a.gated = gated;
+    a.w_scales = scales;
+    a.w_zeros = zeros;
+    a.group = group;
+    a.x_row_bytes = k * 2;
+    a.w_row_bytes = k / 2;
+    a.w_expert_bytes = w_rows * a.w_row_bytes;
+    a.aligned = true;
+    return MX_BOUNDED(stream,
+                      hip_status(mxmoe::launch_grouped_w4(a, static_cast<hipStream_t>(stream))),
+                      Buf{x, num_rows * a.x_row_bytes, false},
+                      Buf{w, num_experts * a.w_expert_bytes, false},
+                      Buf{scales, num_scales * 2, false}, Buf{zeros, num_scales, false},
+                      Buf{expert_offsets, ((int64_t)num_experts + 1) * 4, false},
+                      Buf{problem_sizes, (int64_t)num_experts * 12, false},
+                      Buf{out, num_rows * n * 2, true});
+}
+
+mx_status mx_grouped_gemm_wgrad(const void* grad, const void* x, int32_t dtype, int64_t num_rows,
+                                int32_t num_experts, int64_t n, int64_t k,
+                                const int32_t* expert_offsets, const int32_t* problem_sizes,
+                                void* grad_w, int32_t grad_w_dtype, int32_t accumulate,
+                                void* stream) {
+    if (dtype != MX_F16 && dtype != MX_BF16) return MX_ERR_UNSUPPORTED_DTYPE;
+    const int64_t ob = elem_bytes(grad_w_dtype);
+    if (ob == 0) return MX_ERR_UNSUPPORTED_DTYPE;
+    const mx_status st = check_segments(num_rows, num_experts, n, k, expert_offsets, problem_sizes);
+    if (st != MX_OK) return st;
+    if (grad_w == nullptr || (num_rows > 0 && (grad == nullptr || x == nullptr)))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(grad, 2) || !aligned(x, 2) || !aligned(grad_w, (size_t)ob))
+        return MX_ERR_MISALIGNED;
+    mxmoe::GemmArgs a = product_args(grad, x, grad_w, dtype, grad_w_dtype, num_rows, num_experts,
+                                     k, 1, expert_offsets, problem_sizes);
+    a.out_rows = n;
+    a.x_row_bytes = n * 2;
+    a.w_row_bytes = k * 2;
+    a.accumulate = accumulate != 0;
+    a.aligned = rows16(grad, a.x_row_bytes) && rows16(x, a.w_row_bytes);
+    return MX_BOUNDED(stream,
+                      hip_status(mxmoe::launch_grouped_wgrad(a, static_cast<hipStream_t>(stream))),
+                      Buf{grad, num_rows * a.x_row_bytes, false},
+                      Buf{x, num_rows * a.w_row_bytes, false},
+                      Buf{expert_offsets, ((int64_t)num_experts + 1) * 4, false},
+                      Buf{problem_sizes, (int64_t)num_experts * 12, false},
+                      Buf{grad_w, num_experts * n * k * ob, true});
+}
+
+mx_status mx_silu_mul_backward(const void* grad, const void* gate_up, int32_t dtype,
+                               int64_t num_rows, int32_t num_experts, int64_t n,
+                               const int32_t* expert_offsets, const int32_t* problem_sizes,
+                               void* grad_gate_up, void* stream) {
+    if (dtype != MX_F16 && dtype != MX_BF16) return MX_ERR_UNSUPPORTED_DTYPE;
+    const mx_status st = check_segments(num_rows, num_experts, n, 1, expert_offsets, problem_sizes);
+    if (st != MX_OK) return st;
+    if (num_rows > 0 && (grad == nullptr || gate_up == nullptr || grad_gate_up == nullptr))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(grad, 2) || !aligned(gate_up, 2) || !aligned(grad_gate_up, 2))
+        return MX_ERR_MISALIGNED;
+    if (num_rows == 0) return MX_OK;
+    return MX_BOUNDED(stream,
+                      hip_status(mxmoe::launch_silu_mul_backward(
+                          grad, gate_up, grad_gate_up, dtype, num_rows, n, expert_offsets,
+                          problem_sizes, num_experts, static_cast<hipStream_t>(stream))),
+                      Buf{grad, num_rows * n * 2, false},
+                      Buf{gate_up, num_rows * n * 4, gate_up == grad_gate_up},
+                      Buf{expert_offsets, ((int64_t)num_experts + 1) * 4, false},
+                      Buf{problem_sizes, (int64_t)num_experts * 12, false},
+                      Buf{grad_gate_up, num_rows * n * 4, true});
+}
+
+// ---- top-k gating ------------------------------------------------------------
+
+static mx_status check_gating(const void* logits, int32_t dtype, int64_t num_tokens,
+                              int32_t num_experts, int32_t topk, int32_t scoring,
+                              const void* ids, const void* weights) {
+    if (elem_bytes(dtype) == 0) return MX_ERR_UNSUPPORTED_DTYPE;
+    if (num_tokens < 0 || num_experts < 1 || num_experts > MX_MAX_EXPERTS || topk < 1 ||
+        topk > MX_MAX_TOPK || topk > num_experts || num_tokens > kMax31 / topk ||
+        (scoring != MX_SCORE_SOFTMAX && scoring != MX_SCORE_SIGMOID))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (num_tokens > 0 && (logits == nullptr || ids == nullptr || weights == nullptr))
+        return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(logits, (size_t)elem_bytes(dtype)) || !aligned(ids, 4) || !aligned(weights, 4))
+        return MX_ERR_MISALIGNED;
+    return MX_OK;
+}
+
+mx_status mx_topk_gating(const void* logits, int32_t dtype, int64_t num_tokens,
+                         int32_t num_experts, int32_t topk, int32_t scoring, const float* bias,
+                         int32_t renormalize, float scale, int32_t* topk_ids,
+                         float* topk_weights, void* stream) {
+    const mx_status st = check_gating(logits, dtype, num_tokens, num_experts, topk, scoring,
+                                      topk_ids, topk_weights);
+    if (st != MX_OK) return st;
+    if (bias != nullptr && scoring != MX_SCORE_SIGMOID) return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(bias, 4)) return MX_ERR_MISALIGNED;
+    if (num_tokens == 0) return MX_OK;
+    const mxmoe::GatingArgs a{logits, bias, topk_ids, topk_weights, nullptr, num_tokens,
+                              num_experts, topk, dtype, scoring == MX_SCORE_SIGMOID,
+                              renormalize != 0, scale};
+    return MX_BOUNDED(stream,
+                      hip_status(mxmoe::launch_topk_gating(a, static_cast<hipStream_t>(stream))),
+                      Buf{logits, num_tokens * num_experts * elem_bytes(dtype), false},
+                      Buf{bias, (int64_t)num_experts * 4, false},
+                      Buf{topk_ids, num_tokens * topk * 4, true},
+                      Buf{topk_weights, num_tokens * topk * 4, true});
+}
+
+mx_status mx_topk_gating_backward(const void* logits, int32_t dtype, int64_t num_tokens,
+                                  int32_t num_experts, int32_t topk, int32_t scoring,
+                                  int32_t renormalize, float scale, const int32_t* topk_ids,
+                                  const float* grad_weights, void* grad_logits, void* stream) {
+    const mx_status st = check_gating(logits, dtype, num_tokens, num_experts, topk, scoring,
+                                      topk_ids, grad_weights);
+    if (st != MX_OK) return st;
+    if (num_tokens > 0 && grad_logits == nullptr) return MX_ERR_INVALID_ARGUMENT;
+    if (!aligned(grad_logits, (size_t)elem_bytes(dtype))) return MX_ERR_MISALIGNED;
+    if (num_tokens == 0) return MX_OK;
+    const mxmoe::GatingArgs a{logits, nullptr, const_cast<int32_t*>(topk_ids),
+                              const_cast<float*>(grad_weights), grad_logits, num_tokens,
+                              num_experts, topk, dtype, scoring == MX_SCORE_SIGMOID,
+                              renormalize != 0, scale};
+    return MX_BOUNDED(
+        stream,
+        hip_status(mxmoe::launch_topk_gating_backward(a, static_cast<hipStream_t>(stream))),
+        Buf{logits, num_tokens * num_experts * elem_bytes(dtype), false},
+        Buf{topk_ids, num_tokens * topk * 4, false},
+        Buf{grad_weights, num_tokens * topk * 4, false},
+        Buf{grad_logits, num_tokens * num_experts * elem_bytes(dtype), true});
 }
 
 }  // extern "C"

@@ -135,6 +135,14 @@ enum CheckSite : int {
     kSiteQuantIndex,       // fp8 dispatch: destination row indices
     kSiteQuantCodes,       // fp8 dispatch: code rows
     kSiteQuantScales,      // fp8 dispatch: scale rows
+    kSiteGemmMeta,         // expert products: offsets and row counts
+    kSiteGemmLoad,         // expert products: rows and weights
+    kSiteGemmScale,        // expert products: scales and zero points
+    kSiteGemmOut,          // expert products: output rows, weight gradients
+    kSiteGateLoad,         // gated activation's gradient: inputs
+    kSiteGateOut,          // gated activation's gradient: output rows
+    kSiteTopkLoad,         // top-k gating: logits, bias, ids, weight gradients
+    kSiteTopkOut,          // top-k gating: ids, weights, logit gradients
 };
 
 #ifdef MXMOE_CHECKED

@@ -82,4 +82,58 @@ hipError_t launch_dispatch_quant_fp8(const void* src, int64_t num_tokens, int32_
                                      float* dst_scales, int64_t num_dst_rows,
                                      hipStream_t stream);
 
+// A product grouped by expert (gemm.hip, skinny.hip).  dtype codes as in mxmoe.h.
+struct GemmArgs {
+    const uint8_t* x;         // rows [num_rows][..]; weight gradient: dy rows
+    const uint8_t* w;         // weights [E][..][..]; weight gradient: x rows
+    void* out;
+    void* gate_up;            // gated: both halves before the activation, or null
+    const float* x_scales;    // fp8: [num_rows][len / 128]
+    const void* w_scales;     // fp8: float32 [E][w_scale_rows][len / 128];
+                              // 4 bits: [E][rows of w][len / group] of dtype
+    const uint8_t* w_zeros;   // 4 bits: zero points shaped like w_scales, or null
+    const int32_t* offsets;   // [E + 1]
+    const int32_t* sizes;     // [E][3], the row count first, or null
+    int64_t num_rows;
+    int64_t len;              // contraction length (not of the weight gradient)
+    int64_t out_rows;         // weight gradient: rows of one expert's result
+    int64_t out_cols;
+    int64_t x_row_bytes, w_row_bytes, w_expert_bytes;
+    int32_t w_scale_rows;
+    int32_t group;            // 4 bits: elements of a scale
+    int32_t num_experts;
+    int32_t dtype;            // of x and w (the 4-bit form: of x and the scales)
+    int32_t out_dtype;
+    bool gated;               // w has 2 out_cols rows, gates first
+    bool transposed;          // w is [E][len][out_cols]
+    bool accumulate;          // weight gradient: add to out
+    bool aligned;             // rows of x and w are 16-byte aligned
+    bool vector_store;        // rows of out (and gate_up) take 4-element stores
+};
+
+hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t stream);
+hipError_t launch_grouped_wgrad(const GemmArgs& a, hipStream_t stream);
+hipError_t launch_grouped_w4(const GemmArgs& a, hipStream_t stream);
+
+// Gradient of silu(g) * u on the rows of the segments (gate.hip).
+hipError_t launch_silu_mul_backward(const void* grad, const void* gate_up, void* grad_gate_up,
+                                    int dtype, int64_t num_rows, int64_t n,
+                                    const int32_t* offsets, const int32_t* sizes,
+                                    int32_t num_experts, hipStream_t stream);
+
+// Top-k gating and its gradient (topk.hip).
+struct GatingArgs {
+    const void* logits;       // [T][E] of dtype
+    const float* bias;        // [E] or null
+    int32_t* ids;             // [T][k]; the gradient reads them
+    float* weights;           // [T][k]; the gradient: the weights' gradients, read
+    void* grad_logits;        // [T][E] of dtype
+    int64_t num_tokens;
+    int32_t num_experts, topk, dtype;
+    bool sigmoid, renormalize;
+    float scale;
+};
+hipError_t launch_topk_gating(const GatingArgs& a, hipStream_t stream);
+hipError_t launch_topk_gating_backward(const GatingArgs& a, hipStream_t stream);
+
 }  // namespace mxmoe

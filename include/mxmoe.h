@@ -71,6 +71,17 @@ typedef enum mx_dtype {
  * MX_MAX_EXPERTS counts of 4 bytes). */
 #define MX_NOALLOC_SCRATCH_BYTES (512 * 1024)
 
+/* Most picks of a token mx_topk_gating makes. */
+#define MX_MAX_TOPK 64
+
+/* Scores of mx_topk_gating. */
+#define MX_SCORE_SOFTMAX 0
+#define MX_SCORE_SIGMOID 1
+
+/* Forms of the expert products (flags of mx_grouped_gemm*). */
+#define MX_GEMM_TRANSPOSED 1 /* w is [E][k][n]                                */
+#define MX_GEMM_SILU_MUL 2   /* w is [E][2n][k], out = silu(gate) * up        */
+
 /* Text for a status code (static storage). */
 const char* mx_status_string(mx_status status);
 
@@ -456,6 +467,155 @@ mx_status mx_moe_output_memset(void* out, int64_t num_tokens, int32_t topk, int6
 mx_status mx_zero_padding_rows(void* rows, int64_t num_rows, int64_t row_bytes,
                                const int32_t* input_permutation, const int32_t* expert_offsets,
                                int32_t num_experts, void* stream);
+
+/*
+ * Products of dispatched rows with their expert's weights.
+ *
+ * The calls below work on expert segments: expert e owns the rows from b =
+ * expert_offsets[e] on, c_e of them: problem_sizes[e][0] (the [E][3] array
+ * of mx_prepare_moe_input) but at most expert_offsets[e+1] - b, or all of
+ * those without problem_sizes (NULL).  Both are read on the device; offsets
+ * are clipped to [0, num_rows] and negative counts are none, so no value of
+ * them can make a kernel access memory outside the arrays.  Offsets ascend (as
+ * prepare_moe_input writes them); of others, which rows are computed is not
+ * defined.  Rows outside the segments (padding, unused capacity) are neither
+ * read nor written: they may hold anything, NaN included, before and after.
+ * 1 <= num_experts <= MX_MAX_EXPERTS, num_rows < 2^31, 1 <= n, k <= 2^20.
+ * Outputs must not overlap inputs.  Sums are float32; results do not depend on
+ * what else is in the call.
+ *
+ * grouped_gemm (dtype MX_BF16 or MX_F16, of x and w):
+ *
+ *   out[r][j] = sum_{i < k} x[r][i] * w[e][j][i]          r in segment e
+ *
+ *   x [num_rows, k], w [E, n, k], out [num_rows, n] of out_dtype MX_F32, MX_F16
+ *   or MX_BF16 (rounded once, to nearest even).
+ *   MX_GEMM_TRANSPOSED: w is [E, k, n] and out[r][j] = sum_i x[r][i] * w[e][i][j]:
+ *   with the output gradient of a product as x and that product's weights as
+ *   they are, the gradient of its rows.
+ *   MX_GEMM_SILU_MUL: w is [E, 2n, k], n gate rows and then n up rows (the
+ *   first product of prepare_moe_input's problem sizes), and
+ *     out[r][j] = g / (1 + exp(-g)) * u,  g = x[r] . w[e][j], u = x[r] . w[e][n + j]
+ *   from the unrounded float32 g and u; gate_up [num_rows, 2n] of out_dtype, or
+ *   NULL, takes g and u (rounded) for mx_silu_mul_backward.
+ *   The two flags exclude each other; gate_up goes with MX_GEMM_SILU_MUL only.
+ *   Rows of x and w that are 16-byte aligned (k, and n for w transposed,
+ *   multiples of 8) take the fast path; others work, element by element.
+ */
+mx_status mx_grouped_gemm(const void* x, const void* w, int32_t dtype, int64_t num_rows,
+                          int32_t num_experts, int64_t n, int64_t k, int32_t flags,
+                          const int32_t* expert_offsets, const int32_t* problem_sizes, void* out,
+                          int32_t out_dtype, void* gate_up, void* stream);
+
+/*
+ * grouped_gemm_fp8 -- the same from the rows and scales that
+ * mx_dispatch_rows_fp8 writes, and weights with one scale per 128 x 128 block:
+ *
+ *   out[r][j] = sum_{B < k/128} x_scales[r][B] * w_scales[e][j / 128][B]
+ *                               * sum_{i in block B} x[r][i] * w[e][j][i]
+ *
+ *   x [num_rows, k], w [E, n, k] (2n rows with MX_GEMM_SILU_MUL) OCP e4m3fn
+ *   bytes, 16-byte aligned; x_scales [num_rows, k/128], w_scales
+ *   [E, ceil(rows of w / 128), k/128] float32; out_dtype MX_F16 or MX_BF16.
+ *   k a multiple of 128; with MX_GEMM_SILU_MUL n a multiple of 16.
+ *   Products inside a block are summed by the FP8 matrix instruction, which
+ *   keeps them to about 2^-13 of their absolute sum (measured); sums over
+ *   blocks are float32.  Hence no float32 output.
+ */
+mx_status mx_grouped_gemm_fp8(const void* x, const float* x_scales, const void* w,
+                              const float* w_scales, int64_t num_rows, int32_t num_experts,
+                              int64_t n, int64_t k, int32_t flags, const int32_t* expert_offsets,
+                              const int32_t* problem_sizes, void* out, int32_t out_dtype,
+                              void* stream);
+
+/*
+ * grouped_gemm_w4 -- the same with 4-bit weights, for decoding (few rows to an
+ * expert; any number works, 64 at a time):
+ *
+ *   out[r][j] = sum_i x[r][i] * (q[e][j][i] - z) * s,
+ *   s = scales[e][j][i / group], z = zeros[e][j][i / group] or 8 (zeros NULL)
+ *
+ *   x [num_rows, k] MX_BF16 or MX_F16 (dtype), 16-byte aligned; w
+ *   [E, n, k/2] bytes (2n rows with MX_GEMM_SILU_MUL), 16-byte aligned, q of
+ *   position 2i in the low and of 2i + 1 in the high four bits of byte i;
+ *   scales [E, n, k/group] of dtype, zeros the same shape, one byte each;
+ *   out [num_rows, n] of dtype.  group 32, 64 or 128, k a multiple of it.
+ *   (128 + q) x in bf16, or (1024 + q) x in fp16, is what is summed (and its
+ *   surplus taken off): an infinite x gives NaN.
+ */
+mx_status mx_grouped_gemm_w4(const void* x, int32_t dtype, const void* w, const void* scales,
+                             const uint8_t* zeros, int32_t group, int64_t num_rows,
+                             int32_t num_experts, int64_t n, int64_t k, int32_t flags,
+                             const int32_t* expert_offsets, const int32_t* problem_sizes,
+                             void* out, void* stream);
+
+/*
+ * grouped_gemm_wgrad -- the gradient of a product's weights:
+ *
+ *   grad_w[e][j][i] = sum_{r in segment e} grad[r][j] * x[r][i]   (+ grad_w[e][j][i])
+ *
+ *   grad [num_rows, n], x [num_rows, k] MX_BF16 or MX_F16 (dtype), grad_w
+ *   [E, n, k] of grad_w_dtype MX_F32, MX_F16 or MX_BF16.  accumulate != 0 adds
+ *   to what grad_w holds (in float32, rounded once); otherwise an expert
+ *   without rows gets zeros.
+ */
+mx_status mx_grouped_gemm_wgrad(const void* grad, const void* x, int32_t dtype, int64_t num_rows,
+                                int32_t num_experts, int64_t n, int64_t k,
+                                const int32_t* expert_offsets, const int32_t* problem_sizes,
+                                void* grad_w, int32_t grad_w_dtype, int32_t accumulate,
+                                void* stream);
+
+/*
+ * silu_mul_backward -- the gradient of h = g / (1 + exp(-g)) * u:
+ *
+ *   s = 1 / (1 + exp(-g)):  dg = grad * u * s * (1 + g * (1 - s)),  du = grad * g * s
+ *
+ *   grad [num_rows, n], gate_up [num_rows, 2n] (g, then u), grad_gate_up
+ *   [num_rows, 2n] (dg, then du; may be gate_up itself), MX_BF16 or MX_F16;
+ *   float32 inside, rounded once.
+ */
+mx_status mx_silu_mul_backward(const void* grad, const void* gate_up, int32_t dtype,
+                               int64_t num_rows, int32_t num_experts, int64_t n,
+                               const int32_t* expert_offsets, const int32_t* problem_sizes,
+                               void* grad_gate_up, void* stream);
+
+/*
+ * topk_gating -- a token's experts and their weights from its router logits:
+ * what prepare_moe_input routes by and apply_shuffle_mul_sum weighs with.
+ *
+ *   key[e] = logits[t][e], or sigmoid(logits[t][e]) + bias[e] with a bias
+ *            (computed in float64)
+ *   topk_ids[t]  = the k experts with the largest keys, largest first, equal
+ *                  keys by lower index
+ *   MX_SCORE_SOFTMAX  p_j = exp(l_j) / sum exp(l_i), i over the chosen experts
+ *                     (renormalize != 0) or over all that could be chosen
+ *   MX_SCORE_SIGMOID  p_j = 1 / (1 + exp(-l_j)), divided by the chosen ones' sum
+ *                     (renormalize != 0; 0 where that sum is 0)
+ *   topk_weights[t][j] = scale * p_j
+ *
+ *   An expert whose logit is -inf or NaN (or whose key is) is never chosen;
+ *   places left over hold id -1 (which prepare_moe_input drops) and weight 0.
+ *   Among logits of +inf the softmax weighs those alike and the rest with 0.
+ *   logits [T, E] MX_F32, MX_F16 or MX_BF16; bias [E] float32 or NULL,
+ *   MX_SCORE_SIGMOID only; topk_ids [T, k] int32, topk_weights [T, k] float32;
+ *   1 <= k <= min(E, MX_MAX_TOPK).
+ *
+ * topk_gating_backward -- the gradient of the logits for the ids that
+ * topk_gating chose and the gradient of its weights (same scoring, renormalize
+ * and scale; the selection and the bias have none).  Logits of experts that
+ * were not chosen get 0, but for the softmax over all.  Ids outside [0, E), and
+ * experts with a logit of -inf or NaN, are left out; an id given twice in a
+ * token counts as two picks.  grad_logits [T, E] of dtype.
+ */
+mx_status mx_topk_gating(const void* logits, int32_t dtype, int64_t num_tokens,
+                         int32_t num_experts, int32_t topk, int32_t scoring, const float* bias,
+                         int32_t renormalize, float scale, int32_t* topk_ids,
+                         float* topk_weights, void* stream);
+
+mx_status mx_topk_gating_backward(const void* logits, int32_t dtype, int64_t num_tokens,
+                                  int32_t num_experts, int32_t topk, int32_t scoring,
+                                  int32_t renormalize, float scale, const int32_t* topk_ids,
+                                  const float* grad_weights, void* grad_logits, void* stream);
 
 #ifdef __cplusplus
 }
