@@ -350,6 +350,9 @@ mx_status prepare_moe_input(const void* topk_ids, int32_t ids_dtype, int64_t num
 
 constexpr int64_t kMaxWidth = (int64_t)1 << 20;   // columns and contraction of a product
 
+// n k of a gated product: the up rows lie within 32-bit offsets of the gates.
+constexpr int64_t kMaxGated = (int64_t)1 << 30;
+
 // What every call on expert segments checks: sizes, offsets and row counts.
 mx_status check_segments(int64_t num_rows, int32_t num_experts, int64_t n, int64_t k,
                          const int32_t* expert_offsets, const int32_t* problem_sizes) {
@@ -725,7 +728,7 @@ mx_status mx_grouped_gemm(const void* x, const void* w, int32_t dtype, int64_t n
     if (st != MX_OK) return st;
     const bool gated = flags & MX_GEMM_SILU_MUL, transposed = flags & MX_GEMM_TRANSPOSED;
     if ((flags & ~(MX_GEMM_SILU_MUL | MX_GEMM_TRANSPOSED)) != 0 || (gated && transposed) ||
-        (!gated && gate_up != nullptr))
+        (!gated && gate_up != nullptr) || (gated && n > kMaxGated / k))
         return MX_ERR_INVALID_ARGUMENT;
     if (num_rows > 0 && (x == nullptr || w == nullptr || out == nullptr))
         return MX_ERR_INVALID_ARGUMENT;
@@ -763,7 +766,8 @@ mx_status mx_grouped_gemm_fp8(const void* x, const float* x_scales, const void* 
     const mx_status st = check_segments(num_rows, num_experts, n, k, expert_offsets, problem_sizes);
     if (st != MX_OK) return st;
     const bool gated = flags & MX_GEMM_SILU_MUL;
-    if ((flags & ~MX_GEMM_SILU_MUL) != 0 || k % 128 != 0 || (gated && n % 16 != 0))
+    if ((flags & ~MX_GEMM_SILU_MUL) != 0 || k % 128 != 0 ||
+        (gated && (n % 16 != 0 || n > kMaxGated / k)))
         return MX_ERR_INVALID_ARGUMENT;
     if (num_rows > 0 && (x == nullptr || x_scales == nullptr || w == nullptr ||
                          w_scales == nullptr || out == nullptr))

@@ -10,6 +10,8 @@
 // sizes[e][0] where that is smaller; both are clipped to the arrays, so no
 // value of them makes an access leave the arrays.  Rows outside the segments
 // are neither read nor written.
+#include <type_traits>
+
 #include "device_common.h"
 #include "gemm_common.h"
 #include "launch.h"
@@ -40,9 +42,24 @@ struct Operand {
                              // gate rows and 16 up rows), else 0
 };
 
+// Loads straight to LDS: lane l's 16 bytes at base + soffset + voffset go to LDS
+// address `lds` + 16 l.  Written as assembly because the compiler, which cannot tell
+// the tile being filled from the tile being read, would wait for the loads
+// before the next LDS read; wait_for_loads and a barrier stand where the
+// filled tile is first read.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t voffset,
+                                            uint32_t soffset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voffset), "s"(rs), "s"(soffset), "s"(lds) : "memory");
+}
+
 // The loads to LDS that this wave has issued are done; a barrier by itself
 // does not wait for them.
 __device__ __forceinline__ void wait_for_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+}
 
 // Matrix row of row `r` of a tile.
 template <bool Gated>
@@ -62,43 +79,63 @@ __device__ __forceinline__ int swizzle_across(int kk) {
     return ((kk & 3) | (((kk >> 3) & 1) << 2)) << 1;
 }
 
-// Brings contraction step `step` of an operand into its LDS tile: 32 loads of
-// 1 KiB, four per wave, straight to LDS.  Lane l of a load fills the 16 bytes
-// at position l, so the swizzle is applied to the address it reads.
-// `len`: contraction length in elements; rows, columns and (in the last step)
-// contraction positions past the end read the last ones there are, which
-// zero_tail and the epilogue leave out.
+// An operand's loads: one step is 32 loads of 1 KiB, four per wave.  Lane l of a
+// load fills the 16 bytes at position l of its KiB, so the swizzle is applied
+// to the address it reads.  Rows, columns and (in the last step) contraction
+// positions past the end read the last ones there are, which zero_tail and the
+// epilogue leave out.
 template <Kind K, bool Gated, int ElemBytes>
-__device__ __forceinline__ void stage(const Operand& o, uint8_t* tile, int64_t step, int64_t len,
-                                      int rows_needed) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+struct Loader {
+    // kAcross: loads 2 and 3 are 4 rows below loads 0 and 1, with their swizzle
+    static constexpr int kOffsets = K == kAlong ? 4 : 2;
+    uint32_t voffset[kOffsets];
+    const uint8_t* base;          // of the next step
+    int64_t step_bytes;
+
+    // Contraction positions `valid` (of a step) exist.
+    __device__ __forceinline__ uint32_t offset(const Operand& o, int i, int64_t valid) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
         const int piece = wave * 4 + i;
-        const uint8_t* p;
         if constexpr (K == kAlong) {
-            if (piece * 8 >= rows_needed) continue;
             const int r = piece * 8 + (lane >> 3);
-            const int chunk = (lane & 7) ^ (lane >> 3);
-            int64_t at = step * kStepBytes + chunk * 16;
-            const int64_t last = len * ElemBytes - 16;
+            int32_t at = ((lane & 7) ^ (lane >> 3)) * 16;
+            const int32_t last = (int32_t)valid * ElemBytes - 16;
             at = at < last ? at : last;
-            p = o.base + tile_row<Gated>(o, r) * o.row_bytes + at;
+            return (uint32_t)(tile_row<Gated>(o, r) - o.first) * (uint32_t)o.row_bytes + at;
         } else {
-            const int kk = piece * 2 + (lane >> 5);
+            int kk = piece * 2 + (lane >> 5);
             const int chunk = (lane & 31) ^ swizzle_across(kk);
-            int64_t row = step * 64 + kk;
-            row = row < len ? row : len - 1;
+            kk = kk < valid ? kk : (int)valid - 1;
             int32_t col = o.first + chunk * 8;
             col = col < o.limit ? col : o.limit - 8;
-            p = o.base + row * o.row_bytes + (int64_t)col * 2;
+            return (uint32_t)kk * (uint32_t)o.row_bytes + (uint32_t)(col - o.first) * 2;
         }
-        if (!MX_CAN_LOAD(p, 16, kSiteGemmLoad)) continue;
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)p,
-            (__attribute__((address_space(3))) void*)(tile + piece * 1024), 16, 0, 0);
     }
-}
+    __device__ __forceinline__ void init(const Operand& o) {
+        if constexpr (K == kAlong) {
+            base = o.base + (int64_t)o.first * o.row_bytes;
+            step_bytes = kStepBytes;
+        } else {
+            base = o.base + (int64_t)o.first * 2;
+            step_bytes = 64 * o.row_bytes;
+        }
+#pragma unroll
+        for (int i = 0; i < kOffsets; ++i) voffset[i] = offset(o, i, 1 << 20);
+    }
+    // Load i of the next step, whose `valid` positions exist, into `tile`.
+    template <bool Whole>
+    __device__ __forceinline__ void piece(const Operand& o, const uint8_t* tile, int i,
+                                          int64_t valid) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(base), (short)0, -1, 0x00020000);
+        const uint32_t v = Whole ? voffset[i % kOffsets] : offset(o, i, valid);
+        const uint32_t down = Whole && i >= kOffsets ? 4 * (uint32_t)o.row_bytes : 0u;
+        if (!MX_CAN_LOAD(base + down + v, 16, kSiteGemmLoad)) return;
+        load_to_lds(rs, v, (uint32_t)uniform((int32_t)down), lds_address(tile) + (wave * 4 + i) * 1024);
+    }
+    __device__ __forceinline__ void next() { base += step_bytes; }
+};
 
 // The same for rows that are not 16-byte aligned, element by element, with
 // zeros past every end.
@@ -147,43 +184,63 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
     }
 }
 
-// Fragment of 16 rows x 32 contraction positions (16-bit types) of a staged
-// tile: lane l holds row l & 15, positions 8 (l >> 4) .. + 8 of half `ks`.
-template <Kind K>
-__device__ __forceinline__ u32x4 fragment(const uint8_t* tile, int sub, int ks) {
-    const int lane = threadIdx.x & 63;
-    if constexpr (K == kAlong) {
-        const int chunk = (ks * 4 + (lane >> 4)) ^ (lane & 7);
-        return *reinterpret_cast<const u32x4*>(tile + (sub * 16 + (lane & 15)) * kStepBytes +
-                                               chunk * 16);
-    } else {
-        // ds_read_b64_tr_b16: the 16 lanes of a group read four rows of 16
-        // elements, and lane i gets column i of them.
-        const int g = lane >> 4, j = lane & 15;
-        const int kk = ks * 32 + g * 8 + (j >> 2);
-        const int chunk = (sub * 2 + ((j & 3) >> 1)) ^ swizzle_across(kk);
-        const uint8_t* p = tile + kk * 512 + chunk * 16 + (j & 1) * 8;
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 512));
-        u32x4 r;
-        __builtin_memcpy(&r, &lo, 8);
-        __builtin_memcpy(reinterpret_cast<char*>(&r) + 8, &hi, 8);
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+
+// Fragments of 16 rows x 128 contraction bytes of a staged tile, of the 16-row
+// blocks first + Step i.  Lane l holds row l & 15 of a block: for 16-bit types
+// positions 8 (l >> 4) .. + 8 of each half `ks`, for FP8 positions 32 (l >> 4)
+// .. + 32.  What depends on the lane and not on the block alone is kept in a few
+// LDS addresses (the swizzle's share of a block index is its low three bits);
+// the rest are offsets in the instruction.
+template <Kind K, int Step>
+struct Fragments {
+    uint32_t at[4];
+
+    __device__ __forceinline__ void init(const uint8_t* tile, int first, bool fp8) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
+        const uint32_t base = lds_address(tile);
+        if constexpr (K == kAlong) {
+            const uint32_t row = base + first * 2048 + j * kStepBytes;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                at[i] = row + (((fp8 ? g * 2 + i : i * 4 + g) ^ (lane & 7)) << 4);
+        } else {
+            const int kk = g * 8 + (j >> 2), sw = swizzle_across(kk) >> 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                at[i] = base + kk * 512 + (((first + Step * i) ^ sw) << 5) + (j & 3) * 8;
+        }
+    }
+    // The other of the two tiles.
+    __device__ __forceinline__ void move(int bytes) {
+#pragma unroll
+        for (int i = 0; i < (K == kAlong ? 2 : 4); ++i) at[i] += bytes;
+    }
+    __device__ __forceinline__ u32x4 get(int i, int ks) const {
+        if constexpr (K == kAlong) {
+            return *(lds_u32x4*)(at[ks] + i * Step * 2048);
+        } else {
+            // ds_read_b64_tr_b16: the 16 lanes of a group read four rows of 16
+            // elements, and lane i gets column i of them.
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const uint32_t p = at[i & 3] + (i >> 2) * 4 * Step * 32 + ks * 32 * 512;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 512));
+            u32x4 r;
+            __builtin_memcpy(&r, &lo, 8);
+            __builtin_memcpy(reinterpret_cast<char*>(&r) + 8, &hi, 8);
+            return r;
+        }
+    }
+    __device__ __forceinline__ i32x8 get_fp8(int i) const {
+        const u32x4 lo = get(i, 0), hi = get(i, 1);
+        i32x8 r;
+        __builtin_memcpy(&r, &lo, 16);
+        __builtin_memcpy(reinterpret_cast<char*>(&r) + 16, &hi, 16);
         return r;
     }
-}
-
-// FP8: 16 rows x 128 positions, lane l holds row l & 15, 32 (l >> 4) .. + 32.
-__device__ __forceinline__ i32x8 fragment_fp8(const uint8_t* tile, int sub) {
-    const int lane = threadIdx.x & 63;
-    const uint8_t* row = tile + (sub * 16 + (lane & 15)) * kStepBytes;
-    const int c = (lane >> 4) * 2;
-    i32x8 r;
-    __builtin_memcpy(&r, row + ((c ^ (lane & 7)) << 4), 16);
-    __builtin_memcpy(reinterpret_cast<char*>(&r) + 16, row + (((c + 1) ^ (lane & 7)) << 4), 16);
-    return r;
-}
+};
 
 template <typename T>
 constexpr bool is_fp8() { return __is_same(T, FP8); }
@@ -207,8 +264,53 @@ struct TileJob {
     const float* q_scales;
 };
 
-template <typename T, Mode M, bool Gated, int MI>
-__device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, uint8_t* lds) {
+template <typename T, Mode M, bool Gated>
+struct Loaders {
+    using S = Tiles<T, M, Gated>;
+    Loader<S::kP, false, S::kElem> p;
+    Loader<S::kQ, Gated, S::kElem> q;
+
+    // Readies the loads of a tile and, where its rows are aligned, sets off
+    // those of the first step.
+    __device__ __forceinline__ void start(const GemmArgs& a, const TileJob& job, uint8_t* lds) {
+        if (!a.aligned || job.len <= 0) return;
+        p.init(job.p);
+        q.init(job.q);
+        all<8>(job, lds, 0);
+    }
+    // Load i of 8 of step s.  A wave's four loads of the m operand are 32 rows:
+    // those past a smaller tile's MI x 32 are left out.
+    template <bool Whole, int MI>
+    __device__ __forceinline__ void piece(const TileJob& job, uint8_t* lds, int64_t s, int i) {
+        const int64_t valid = job.len - s * S::kStep;
+        uint8_t* tile = lds + (s & 1) * kTileBytes;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        if (i >= 4) q.template piece<Whole>(job.q, tile + 2 * kTileBytes, i - 4, valid);
+        else if (MI == 8 || S::kP == kAcross || wave < MI)
+            p.template piece<Whole>(job.p, tile, i, valid);
+    }
+    template <int MI>
+    __device__ __forceinline__ void all(const TileJob& job, uint8_t* lds, int64_t s) {
+        if (job.len - s * S::kStep >= S::kStep) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) piece<true, MI>(job, lds, s, i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) piece<false, MI>(job, lds, s, i);
+        }
+        next();
+    }
+    __device__ __forceinline__ void next() {
+        p.next();
+        q.next();
+    }
+};
+
+// One tile; its first step's loads are under way.  `advance` sets off the next
+// tile's, between the sums and the stores.
+template <typename T, Mode M, bool Gated, int MI, typename F>
+__device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, uint8_t* lds,
+                                         Loaders<T, M, Gated>& loads, F&& advance) {
     using S = Tiles<T, M, Gated>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave & 1, wn = wave >> 1;
@@ -218,32 +320,20 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int64_t steps = (job.len + S::kStep - 1) / S::kStep;
-    uint8_t* tp = lds;                                  // two tiles of the m operand,
-    uint8_t* tq = lds + 2 * kTileBytes;                 // two of the n operand
-    const int p_rows = MI * 32;
-    auto bring = [&](int64_t s) {
-        const int b = (int)(s & 1) * kTileBytes;
-        if (a.aligned || is_fp8<T>()) {
-            stage<S::kP, false, S::kElem>(job.p, tp + b, s, job.len, p_rows);
-            stage<S::kQ, Gated, S::kElem>(job.q, tq + b, s, job.len, kTileN);
-        } else if constexpr (!is_fp8<T>()) {
-            stage_elements<S::kP, false>(job.p, tp + b, s, job.len);
-            stage_elements<S::kQ, Gated>(job.q, tq + b, s, job.len);
-        }
-    };
-    if (steps > 0) bring(0);
-    for (int64_t s = 0; s < steps; ++s) {
-        wait_for_loads();
-        __syncthreads();                                // tile s is there, tile s - 1 is read
-        const int b = (int)(s & 1) * kTileBytes;
-        const int64_t rest = job.len - s * S::kStep;
-        if (!is_fp8<T>() && rest < S::kStep && a.aligned) {
-            zero_tail<S::kP>(tp + b, (int)rest);
-            zero_tail<S::kQ>(tq + b, (int)rest);
-            __syncthreads();
-        }
-        if (s + 1 < steps) bring(s + 1);
+    const bool aligned = a.aligned || is_fp8<T>();
+    Fragments<S::kP, 2> fp;
+    Fragments<S::kQ, 1> fq;
+    fp.init(lds, wm, is_fp8<T>());
+    fq.init(lds + 2 * kTileBytes, wn * 4, is_fp8<T>());
+    // The products of one step from its tiles; Load: with the loads of step
+    // s + 1 (a whole one) in between.
+    auto multiply = [&](int64_t s, auto load) {
+        constexpr bool kLoad = decltype(load)::value;
         if constexpr (is_fp8<T>()) {
+            if (kLoad) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) loads.template piece<true, MI>(job, lds, s + 1, i);
+            }
             // one step is one scale block: its product, unscaled, then a
             // float32 multiply-add with both scales
             float sq[Gated ? 4 : 1];
@@ -256,14 +346,14 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
             }
             i32x8 q[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = fragment_fp8(tq + b, wn * 4 + j);
+            for (int j = 0; j < 4; ++j) q[j] = fq.get_fp8(j);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int32_t m = (i * 2 + wm) * 16 + (lane & 15);
                 const int32_t mc = m < job.m_rows ? m : job.m_rows - 1;
                 const float* ps = job.p_scales + (int64_t)mc * kb + s;
                 const float sp = MX_CAN_LOAD(ps, 4, kSiteGemmScale) ? *ps : 0.0f;
-                const i32x8 p = fragment_fp8(tp + b, i * 2 + wm);
+                const i32x8 p = fp.get_fp8(i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const f32x4 part = mfma_fp8(q[j], p, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
@@ -273,21 +363,71 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                 }
             }
         } else {
+            // 2 MI turns of one m fragment and four matrix instructions: the
+            // fragment two turns ahead, the n fragments of the second half and
+            // the next step's loads are issued in between, in this order.
+            u32x4 q[2][4], p[3];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                u32x4 q[4];
+            for (int j = 0; j < 4; ++j) q[0][j] = fq.get(j, 0);
+            p[0] = fp.get(0, 0);
+            p[1] = fp.get(1 % MI, 1 / MI);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = fragment<S::kQ>(tq + b, wn * 4 + j, ks);
+            for (int t = 0; t < 2 * MI; ++t) {
+                if (t + 2 < 2 * MI) p[(t + 2) % 3] = fp.get((t + 2) % MI, (t + 2) / MI);
+                if (t < MI) {
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    const u32x4 p = fragment<S::kP>(tp + b, i * 2 + wm, ks);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16(T{}, q[j], p, acc[i][j]);
+                    for (int j = 0; j < 4; ++j)
+                        if (j * MI / 4 == t) q[1][j] = fq.get(j, 1);
                 }
+                if (kLoad) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i * MI / 8 == t) loads.template piece<true, MI>(job, lds, s + 1, i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[t % MI][j] = mfma_16(T{}, q[t / MI][j], p[t % 3], acc[t % MI][j]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        if (kLoad) loads.next();
+        if (aligned) {
+            const int other = (s & 1) ? -kTileBytes : kTileBytes;
+            fp.move(other);
+            fq.move(other);
+        }
+    };
+    if (aligned) {
+        const int64_t whole = job.len / S::kStep;
+        int64_t s = 0;
+        for (; s + 1 < whole; ++s) {
+            wait_for_loads();
+            __syncthreads();                            // step s is there, step s - 1 is read
+            multiply(s, std::true_type{});
+        }
+        for (; s < steps; ++s) {                        // the last whole step and a partial one
+            wait_for_loads();
+            __syncthreads();
+            if (s == whole) {
+                zero_tail<S::kP>(lds + (s & 1) * kTileBytes, (int)(job.len - s * S::kStep));
+                zero_tail<S::kQ>(lds + (2 + (s & 1)) * kTileBytes, (int)(job.len - s * S::kStep));
+                __syncthreads();
+            }
+            if (s + 1 < steps) loads.template all<MI>(job, lds, s + 1);
+            multiply(s, std::false_type{});
+        }
+    } else if constexpr (!is_fp8<T>()) {
+        for (int64_t s = 0; s < steps; ++s) {
+            __syncthreads();
+            stage_elements<S::kP, false>(job.p, lds, s, job.len);
+            stage_elements<S::kQ, Gated>(job.q, lds + 2 * kTileBytes, s, job.len);
+            __syncthreads();
+            multiply(0, std::false_type{});
+        }
     }
-    __syncthreads();                                    // the next tile's loads may begin
+    __syncthreads();                                    // the tiles are read
+    advance();
     // Lane l holds columns 4 (l >> 4) .. + 4 of row l & 15 of each 16 x 16 block.
     const int64_t n = a.out_cols;
 #pragma unroll
@@ -333,17 +473,17 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_rows_kernel(GemmArgs a) {
     count_row_tiles<kThreads>(a, first_tile, wave_total, m_tiles);
     const int32_t cols_per_tile = Gated ? kTileN / 2 : kTileN;
     const int32_t n_tiles = (int32_t)((a.out_cols + cols_per_tile - 1) / cols_per_tile);
-    const int64_t total = (int64_t)first_tile[a.num_experts] * n_tiles;
+    const int64_t total = (int64_t)uniform(first_tile[a.num_experts]) * n_tiles;
     // Workgroup b runs on XCD b % 8: each XCD takes a contiguous eighth of the tiles.
     const int64_t per = (total + kXcds - 1) / kXcds;
     const int64_t begin = per * (blockIdx.x % kXcds);
     const int64_t end = begin + per < total ? begin + per : total;
     int e = 0;
-    for (int64_t t = begin + blockIdx.x / kXcds; t < end; t += gridDim.x / kXcds) {
+    auto job_of = [&](int64_t t) {
         e = expert_of_tile(first_tile, a.num_experts, n_tiles, t, e);
-        const Segment sg = segment(a, e);
+        const Segment sg = uniform_segment(a, e);
         const int32_t mt = m_tiles(sg.count);
-        const int64_t r = t - (int64_t)first_tile[e] * n_tiles;
+        const int64_t r = t - (int64_t)uniform(first_tile[e]) * n_tiles;
         // groups of at most 8 row tiles, rows fastest inside a group
         const int32_t per_group = 8 * n_tiles;
         const int32_t group = (int32_t)(r / per_group);
@@ -354,24 +494,41 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_rows_kernel(GemmArgs a) {
         // the segment's rows are spread over its tiles in multiples of 64
         const int32_t step = ((sg.count + mt - 1) / mt + 63) / 64 * 64;
         const int64_t m0 = (int64_t)m_tile * step;
-        const int32_t rows = (int32_t)(sg.count - m0 < step ? sg.count - m0 : step);
-        if (rows <= 0) continue;
         TileJob job;
-        job.p = Operand{a.x + (sg.begin + m0) * a.x_row_bytes, a.x_row_bytes, 0, rows, 0};
+        job.m_rows = (int32_t)(sg.count - m0 < step ? sg.count - m0 : step);
+        job.p = Operand{a.x + (sg.begin + m0) * a.x_row_bytes, a.x_row_bytes, 0, job.m_rows, 0};
         job.q = Operand{a.w + (int64_t)e * a.w_expert_bytes, a.w_row_bytes,
                         n_tile * cols_per_tile, (int32_t)a.out_cols,
                         Gated ? (int32_t)a.out_cols : 0};
         job.len = a.len;
-        job.m_rows = rows;
         job.out_row0 = sg.begin + m0;
         if constexpr (is_fp8<T>()) {
             job.p_scales = a.x_scales + (sg.begin + m0) * (a.len / 128);
-            job.q_scales = static_cast<const float*>(a.w_scales) + (int64_t)e * a.w_scale_rows * (a.len / 128);
+            job.q_scales = static_cast<const float*>(a.w_scales) +
+                           (int64_t)e * a.w_scale_rows * (a.len / 128);
         }
-        if (rows <= 64) run_tile<T, M, Gated, 2>(a, job, lds);
-        else if (rows <= 128) run_tile<T, M, Gated, 4>(a, job, lds);
-        else if (rows <= 192) run_tile<T, M, Gated, 6>(a, job, lds);
-        else run_tile<T, M, Gated, 8>(a, job, lds);
+        return job;
+    };
+    int64_t t = begin + blockIdx.x / kXcds;
+    if (t >= end) return;
+    Loaders<T, M, Gated> loads;
+    TileJob job = job_of(t);
+    loads.start(a, job, lds);
+    while (true) {
+        const int64_t next = t + gridDim.x / kXcds;
+        TileJob next_job;
+        auto advance = [&]() {
+            if (next >= end) return;
+            next_job = job_of(next);
+            loads.start(a, next_job, lds);
+        };
+        if (job.m_rows <= 64) run_tile<T, M, Gated, 2>(a, job, lds, loads, advance);
+        else if (job.m_rows <= 128) run_tile<T, M, Gated, 4>(a, job, lds, loads, advance);
+        else if (job.m_rows <= 192) run_tile<T, M, Gated, 6>(a, job, lds, loads, advance);
+        else run_tile<T, M, Gated, 8>(a, job, lds, loads, advance);
+        if (next >= end) return;
+        t = next;
+        job = next_job;
     }
 }
 
@@ -386,24 +543,41 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_weight_grad_kernel(GemmArgs 
     const int xcd = blockIdx.x % kXcds;
     const int64_t per = (tiles + kXcds - 1) / kXcds;    // each XCD: the same tiles of every expert
     const int64_t total = per * a.num_experts;
-    for (int64_t t = blockIdx.x / kXcds; t < total; t += gridDim.x / kXcds) {
-        const int32_t e = (int32_t)(t / per);
-        const int64_t at = xcd * per + (t - e * per);
-        if (at >= tiles) continue;
-        const int32_t n_tile = (int32_t)(at / mt), m_tile = (int32_t)(at - (int64_t)n_tile * mt);
-        const Segment sg = segment(a, e);
-        if (sg.count == 0 && a.accumulate) continue;
-        TileJob job;
-        job.p = Operand{a.x + sg.begin * a.x_row_bytes, a.x_row_bytes, m_tile * kTileM,
-                        (int32_t)a.out_rows, 0};
-        job.q = Operand{a.w + sg.begin * a.w_row_bytes, a.w_row_bytes, n_tile * kTileN,
-                        (int32_t)a.out_cols, 0};
-        job.len = sg.count;
-        job.m_rows = (int32_t)(a.out_rows - (int64_t)m_tile * kTileM < kTileM
-                                   ? a.out_rows - (int64_t)m_tile * kTileM : kTileM);
-        job.out_row0 = (int64_t)e * a.out_rows + (int64_t)m_tile * kTileM;
-        job.p_scales = job.q_scales = nullptr;
-        run_tile<T, kWeightGrad, false, 8>(a, job, lds);
+    int64_t t = blockIdx.x / kXcds;
+    // the next tile of this workgroup, from t on; false: none
+    auto find = [&](TileJob& job) {
+        for (; t < total; t += gridDim.x / kXcds) {
+            const int32_t e = (int32_t)(t / per);
+            const int64_t at = xcd * per + (t - e * per);
+            const Segment sg = uniform_segment(a, e);
+            if (at >= tiles || (sg.count == 0 && a.accumulate)) continue;
+            const int32_t n_tile = (int32_t)(at / mt), m_tile = (int32_t)(at - (int64_t)n_tile * mt);
+            job.p = Operand{a.x + sg.begin * a.x_row_bytes, a.x_row_bytes, m_tile * kTileM,
+                            (int32_t)a.out_rows, 0};
+            job.q = Operand{a.w + sg.begin * a.w_row_bytes, a.w_row_bytes, n_tile * kTileN,
+                            (int32_t)a.out_cols, 0};
+            job.len = sg.count;
+            job.m_rows = (int32_t)(a.out_rows - (int64_t)m_tile * kTileM < kTileM
+                                       ? a.out_rows - (int64_t)m_tile * kTileM : kTileM);
+            job.out_row0 = (int64_t)e * a.out_rows + (int64_t)m_tile * kTileM;
+            return true;
+        }
+        return false;
+    };
+    Loaders<T, kWeightGrad, false> loads;
+    TileJob job;
+    if (!find(job)) return;
+    loads.start(a, job, lds);
+    while (true) {
+        TileJob next_job;
+        bool more = false;
+        run_tile<T, kWeightGrad, false, 8>(a, job, lds, loads, [&]() {
+            t += gridDim.x / kXcds;
+            more = find(next_job);
+            if (more) loads.start(a, next_job, lds);
+        });
+        if (!more) return;
+        job = next_job;
     }
 }
 

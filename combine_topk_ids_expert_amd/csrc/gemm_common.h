@@ -16,6 +16,9 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// A wave-uniform value, kept in scalar registers.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
 struct Segment {
     int64_t begin;
     int32_t count;
@@ -38,6 +41,12 @@ __device__ __forceinline__ Segment segment(const int32_t* offsets, const int32_t
 
 __device__ __forceinline__ Segment segment(const GemmArgs& a, int e) {
     return segment(a.offsets, a.sizes, a.num_rows, e);
+}
+
+// The same for an expert that is the same in the whole wave (rows are below 2^31).
+__device__ __forceinline__ Segment uniform_segment(const GemmArgs& a, int e) {
+    const Segment s = segment(a, e);
+    return Segment{(int64_t)uniform((int32_t)s.begin), uniform(s.count)};
 }
 
 // D = A x B + C for A, B of 16 rows x 32 positions; lane l of the result holds

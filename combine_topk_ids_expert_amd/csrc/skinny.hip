@@ -221,16 +221,16 @@ __global__ __launch_bounds__(kThreads) void skinny_kernel(GemmArgs a) {
     count_row_tiles<kThreads>(a, first_tile, wave_total, row_tiles);
     const int32_t cols_per_tile = Gated ? kCols / 2 : kCols;
     const int32_t n_tiles = (int32_t)((a.out_cols + cols_per_tile - 1) / cols_per_tile);
-    const int64_t total = (int64_t)first_tile[a.num_experts] * n_tiles;
+    const int64_t total = (int64_t)uniform(first_tile[a.num_experts]) * n_tiles;
     const int64_t per = (total + kXcds - 1) / kXcds;
     const int64_t begin = per * (blockIdx.x % kXcds);
     const int64_t end = begin + per < total ? begin + per : total;
     int e = 0;
     for (int64_t t = begin + blockIdx.x / kXcds; t < end; t += gridDim.x / kXcds) {
         e = expert_of_tile(first_tile, a.num_experts, n_tiles, t, e);
-        const Segment sg = segment(a, e);
+        const Segment sg = uniform_segment(a, e);
         const int32_t mt = row_tiles(sg.count);
-        const int64_t r = t - (int64_t)first_tile[e] * n_tiles;
+        const int64_t r = t - (int64_t)uniform(first_tile[e]) * n_tiles;
         const int32_t n_tile = (int32_t)(r / mt), m_tile = (int32_t)(r - (int64_t)n_tile * mt);
         const int64_t row0 = sg.begin + (int64_t)m_tile * kRows;
         const int rows = sg.count - m_tile * kRows < kRows ? sg.count - m_tile * kRows : kRows;

@@ -494,7 +494,7 @@ mx_status mx_zero_padding_rows(void* rows, int64_t num_rows, int64_t row_bytes,
  *   with the output gradient of a product as x and that product's weights as
  *   they are, the gradient of its rows.
  *   MX_GEMM_SILU_MUL: w is [E, 2n, k], n gate rows and then n up rows (the
- *   first product of prepare_moe_input's problem sizes), and
+ *   first product of prepare_moe_input's problem sizes), n k at most 2^30, and
  *     out[r][j] = g / (1 + exp(-g)) * u,  g = x[r] . w[e][j], u = x[r] . w[e][n + j]
  *   from the unrounded float32 g and u; gate_up [num_rows, 2n] of out_dtype, or
  *   NULL, takes g and u (rounded) for mx_silu_mul_backward.
