@@ -363,6 +363,8 @@ mx_status check_segments(int64_t num_rows, int32_t num_experts, int64_t n, int64
     return MX_OK;
 }
 
+bool rows16(const void* p, int64_t row_bytes) { return aligned(p, 16) && row_bytes % 16 == 0; }
+
 mxmoe::GemmArgs product_args(const void* x, const void* w, void* out, int32_t dtype,
                              int32_t out_dtype, int64_t num_rows, int32_t num_experts, int64_t n,
                              int64_t k, const int32_t* expert_offsets,
@@ -379,11 +381,9 @@ mxmoe::GemmArgs product_args(const void* x, const void* w, void* out, int32_t dt
     a.num_experts = num_experts;
     a.dtype = dtype;
     a.out_dtype = out_dtype;
-    a.vector_store = n % 4 == 0 && aligned(out, 4 * (size_t)elem_bytes(out_dtype));
+    a.vector_store = rows16(out, n * elem_bytes(out_dtype));
     return a;
 }
-
-bool rows16(const void* p, int64_t row_bytes) { return aligned(p, 16) && row_bytes % 16 == 0; }
 
 }  // namespace
 
@@ -746,7 +746,7 @@ mx_status mx_grouped_gemm(const void* x, const void* w, int32_t dtype, int64_t n
     a.w_row_bytes = (transposed ? n : k) * 2;
     a.w_expert_bytes = w_rows * a.w_row_bytes;
     a.aligned = rows16(x, a.x_row_bytes) && rows16(w, a.w_row_bytes);
-    a.vector_store = a.vector_store && aligned(gate_up, 4 * (size_t)ob);
+    a.vector_store = a.vector_store && aligned(gate_up, 16);
     return MX_BOUNDED(stream,
                       hip_status(mxmoe::launch_grouped_gemm(a, static_cast<hipStream_t>(stream))),
                       Buf{x, num_rows * a.x_row_bytes, false},

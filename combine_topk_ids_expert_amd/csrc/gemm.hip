@@ -19,8 +19,13 @@
 namespace mxmoe {
 namespace {
 
-constexpr int kThreads = 512;             // 8 waves: 2 along m, 4 along n
+// Four waves, 2 x 2, of up to 128 x 128 results each.  A wave of that size
+// reads 32 KiB of fragments from LDS per step; eight waves of 128 x 64 would
+// read 192 KiB together in place of 128, as long as their matrix instructions
+// take.
+constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr int kTileM = 256, kTileN = 256;
+constexpr int NI = 8;                     // 16-column blocks of a wave
 constexpr int kStepBytes = 128;           // contraction bytes of one step, a tile row in LDS
 constexpr int kTileBytes = 256 * kStepBytes;
 constexpr int kXcds = 8;
@@ -79,15 +84,15 @@ __device__ __forceinline__ int swizzle_across(int kk) {
     return ((kk & 3) | (((kk >> 3) & 1) << 2)) << 1;
 }
 
-// An operand's loads: one step is 32 loads of 1 KiB, four per wave.  Lane l of a
-// load fills the 16 bytes at position l of its KiB, so the swizzle is applied
-// to the address it reads.  Rows, columns and (in the last step) contraction
-// positions past the end read the last ones there are, which zero_tail and the
-// epilogue leave out.
+// An operand's loads: one step is 32 loads of 1 KiB, eight per wave, and load i
+// of wave w is KiB 4 i + w of the tile.  Lane l of a load fills the 16 bytes at
+// position l of its KiB, so the swizzle is applied to the address it reads.
+// Rows, columns and (in the last step) contraction positions past the end read
+// the last ones there are, which zero_tail and the epilogue leave out.
 template <Kind K, bool Gated, int ElemBytes>
 struct Loader {
-    // kAcross: loads 2 and 3 are 4 rows below loads 0 and 1, with their swizzle
-    static constexpr int kOffsets = K == kAlong ? 4 : 2;
+    // kAcross: loads i + 2, ... are 16 rows below load i, with its swizzle
+    static constexpr int kOffsets = K == kAlong ? 8 : 2;
     uint32_t voffset[kOffsets];
     const uint8_t* base;          // of the next step
     int64_t step_bytes;
@@ -95,15 +100,15 @@ struct Loader {
     // Contraction positions `valid` (of a step) exist.
     __device__ __forceinline__ uint32_t offset(const Operand& o, int i, int64_t valid) const {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-        const int piece = wave * 4 + i;
+        const int kib = i * kWaves + wave;
         if constexpr (K == kAlong) {
-            const int r = piece * 8 + (lane >> 3);
+            const int r = kib * 8 + (lane >> 3);
             int32_t at = ((lane & 7) ^ (lane >> 3)) * 16;
             const int32_t last = (int32_t)valid * ElemBytes - 16;
             at = at < last ? at : last;
             return (uint32_t)(tile_row<Gated>(o, r) - o.first) * (uint32_t)o.row_bytes + at;
         } else {
-            int kk = piece * 2 + (lane >> 5);
+            int kk = kib * 2 + (lane >> 5);
             const int chunk = (lane & 31) ^ swizzle_across(kk);
             kk = kk < valid ? kk : (int)valid - 1;
             int32_t col = o.first + chunk * 8;
@@ -130,9 +135,10 @@ struct Loader {
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<uint8_t*>(base), (short)0, -1, 0x00020000);
         const uint32_t v = Whole ? voffset[i % kOffsets] : offset(o, i, valid);
-        const uint32_t down = Whole && i >= kOffsets ? 4 * (uint32_t)o.row_bytes : 0u;
+        const uint32_t down = Whole ? i / kOffsets * 16 * (uint32_t)o.row_bytes : 0u;
         if (!MX_CAN_LOAD(base + down + v, 16, kSiteGemmLoad)) return;
-        load_to_lds(rs, v, (uint32_t)uniform((int32_t)down), lds_address(tile) + (wave * 4 + i) * 1024);
+        load_to_lds(rs, v, (uint32_t)uniform((int32_t)down),
+                    lds_address(tile) + (i * kWaves + wave) * 1024);
     }
     __device__ __forceinline__ void next() { base += step_bytes; }
 };
@@ -142,9 +148,11 @@ struct Loader {
 template <Kind K, bool Gated>
 __device__ __forceinline__ void stage_elements(const Operand& o, uint8_t* tile, int64_t step,
                                                int64_t len) {
-    for (int i = 0; i < 4; ++i) {
-        const int piece = i * 512 + threadIdx.x;            // 16 bytes of the tile
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const int piece = i * kThreads + threadIdx.x;       // 16 bytes of the tile
         uint32_t v[4];
+#pragma unroll
         for (int d = 0; d < 4; ++d) {
             uint32_t word = 0;
             for (int h = 0; h < 2; ++h) {
@@ -175,8 +183,9 @@ __device__ __forceinline__ void stage_elements(const Operand& o, uint8_t* tile, 
 // Zeros at the contraction positions past `valid` (< 64) of a staged tile.
 template <Kind K>
 __device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
-    for (int i = 0; i < 4; ++i) {
-        const int piece = i * 512 + threadIdx.x;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        const int piece = i * kThreads + threadIdx.x;
         bool past;
         if constexpr (K == kAlong) past = ((piece & 7) ^ ((piece >> 3) & 7)) * 8 >= valid;
         else past = (piece >> 5) >= valid;
@@ -184,6 +193,7 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
     }
 }
 
+typedef __attribute__((address_space(3))) const uint8_t lds_byte;
 typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 
 // Fragments of 16 rows x 128 contraction bytes of a staged tile, of the 16-row
@@ -194,27 +204,29 @@ typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 // the rest are offsets in the instruction.
 template <Kind K, int Step>
 struct Fragments {
-    uint32_t at[4];
+    // blocks whose index differs in its low three bits alone
+    static constexpr int kAt = K == kAlong ? 2 : 8 / Step;
+    lds_byte* at[kAt];
 
     __device__ __forceinline__ void init(const uint8_t* tile, int first, bool fp8) {
         const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
-        const uint32_t base = lds_address(tile);
+        lds_byte* const base = (lds_byte*)tile;
         if constexpr (K == kAlong) {
-            const uint32_t row = base + first * 2048 + j * kStepBytes;
+            lds_byte* const row = base + first * 2048 + j * kStepBytes;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 at[i] = row + (((fp8 ? g * 2 + i : i * 4 + g) ^ (lane & 7)) << 4);
         } else {
             const int kk = g * 8 + (j >> 2), sw = swizzle_across(kk) >> 1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kAt; ++i)
                 at[i] = base + kk * 512 + (((first + Step * i) ^ sw) << 5) + (j & 3) * 8;
         }
     }
     // The other of the two tiles.
     __device__ __forceinline__ void move(int bytes) {
 #pragma unroll
-        for (int i = 0; i < (K == kAlong ? 2 : 4); ++i) at[i] += bytes;
+        for (int i = 0; i < kAt; ++i) at[i] += bytes;
     }
     __device__ __forceinline__ u32x4 get(int i, int ks) const {
         if constexpr (K == kAlong) {
@@ -224,7 +236,7 @@ struct Fragments {
             // elements, and lane i gets column i of them.
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const uint32_t p = at[i & 3] + (i >> 2) * 4 * Step * 32 + ks * 32 * 512;
+            lds_byte* const p = at[i % kAt] + i / kAt * 8 * 32 + ks * 32 * 512;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 512));
             u32x4 r;
@@ -270,33 +282,40 @@ struct Loaders {
     Loader<S::kP, false, S::kElem> p;
     Loader<S::kQ, Gated, S::kElem> q;
 
+    // Loads of the m operand of a tile of 32 MI rows.
+    static constexpr int m_loads(int MI) { return S::kP == kAlong ? MI : 8; }
+
     // Readies the loads of a tile and, where its rows are aligned, sets off
-    // those of the first step.
+    // those of its first step, and of the second if both are whole (FP8: of
+    // the first).
     __device__ __forceinline__ void start(const GemmArgs& a, const TileJob& job, uint8_t* lds) {
         if (!a.aligned || job.len <= 0) return;
         p.init(job.p);
         q.init(job.q);
-        all<8>(job, lds, 0);
+        step(job, lds, 0);
+        if (!is_fp8<T>() && job.len >= 2 * S::kStep) step(job, lds, 1);
     }
-    // Load i of 8 of step s.  A wave's four loads of the m operand are 32 rows:
-    // those past a smaller tile's MI x 32 are left out.
-    template <bool Whole, int MI>
-    __device__ __forceinline__ void piece(const TileJob& job, uint8_t* lds, int64_t s, int i) {
+    // Load i of step s: first the m operand's, then the eight of the n operand.
+    template <bool Whole>
+    __device__ __forceinline__ void piece(const TileJob& job, uint8_t* lds, int64_t s, int i,
+                                          int m_loads) {
         const int64_t valid = job.len - s * S::kStep;
         uint8_t* tile = lds + (s & 1) * kTileBytes;
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        if (i >= 4) q.template piece<Whole>(job.q, tile + 2 * kTileBytes, i - 4, valid);
-        else if (MI == 8 || S::kP == kAcross || wave < MI)
-            p.template piece<Whole>(job.p, tile, i, valid);
+        if (i >= m_loads) q.template piece<Whole>(job.q, tile + 2 * kTileBytes, i - m_loads, valid);
+        else p.template piece<Whole>(job.p, tile, i, valid);
     }
-    template <int MI>
-    __device__ __forceinline__ void all(const TileJob& job, uint8_t* lds, int64_t s) {
-        if (job.len - s * S::kStep >= S::kStep) {
+    // All loads of step s, the next one.
+    __device__ __forceinline__ void step(const TileJob& job, uint8_t* lds, int64_t s) {
+        const bool whole = job.len - s * S::kStep >= S::kStep;
+        const int rows = (job.m_rows + 63) / 64 * 64;
+        if (whole) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) piece<true, MI>(job, lds, s, i);
+            for (int i = 0; i < 16; ++i)
+                if (i >= 8 || S::kP == kAcross || i * 32 < rows) piece<true>(job, lds, s, i, 8);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) piece<false, MI>(job, lds, s, i);
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i)
+                if (i >= 8 || S::kP == kAcross || i * 32 < rows) piece<false>(job, lds, s, i, 8);
         }
         next();
     }
@@ -306,47 +325,141 @@ struct Loaders {
     }
 };
 
-// One tile; its first step's loads are under way.  `advance` sets off the next
-// tile's, between the sums and the stores.
+// Writes a tile's results.  They pass through LDS, 16 rows x 64 columns of a
+// wave at a time, so that each row is written in pieces of 64 to 256 bytes.
+// Lane l of a result holds columns 4 (l >> 4) .. + 4 of row l & 15 of a block.
+constexpr int kStageRow = 64 + 4;                       // floats; the rest spreads the banks
+constexpr int kStageBytes = kWaves * 16 * kStageRow * 4;
+
+template <typename OT, Mode M, bool Gated, int MI>
+__device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job,
+                                           const f32x4 (&acc)[MI][NI], float* stage, int wm,
+                                           int wn) {
+    using E = typename OT::storage;
+    constexpr int kChunk = 16 / (int)sizeof(E);         // elements of a 16-byte store
+    struct alignas(16) Chunk { E e[kChunk]; };
+    const int lane = threadIdx.x & 63;
+    const int64_t n = a.out_cols;
+    // 16 rows x `cols` columns from stage columns at(0 .. cols) to row0, col0
+    auto put = [&](void* base, int64_t width, int64_t row0, int64_t col0, int64_t limit, int rows,
+                   auto cols, auto value) {
+        constexpr int kCols = decltype(cols)::value;
+        if (a.vector_store) {
+            const int r = lane >> 2;
+            E* p = static_cast<E*>(base) + (row0 + r) * width + col0;
+#pragma unroll
+            for (int i = 0; i < kCols / 4; i += kChunk) {
+                const int c = (lane & 3) * (kCols / 4) + i;
+                if (r >= rows || col0 + c >= limit || !MX_CAN_STORE(p + c, 16, kSiteGemmOut))
+                    continue;
+                Chunk v;
+                if (M == kWeightGrad && a.accumulate) {
+                    v = *reinterpret_cast<const Chunk*>(p + c);
+#pragma unroll
+                    for (int d = 0; d < kChunk; ++d)
+                        v.e[d] = from_f32(OT{}, value(r, c + d) + to_f32(OT{}, v.e[d]));
+                } else {
+#pragma unroll
+                    for (int d = 0; d < kChunk; ++d) v.e[d] = from_f32(OT{}, value(r, c + d));
+                }
+                *reinterpret_cast<Chunk*>(p + c) = v;
+            }
+        } else {
+#pragma unroll 1
+            for (int at = lane; at < 16 * kCols; at += kWave) {
+                const int r = at / kCols, c = at % kCols;
+                E* p = static_cast<E*>(base) + (row0 + r) * width + col0 + c;
+                if (r >= rows || col0 + c >= limit || !MX_CAN_STORE(p, sizeof(E), kSiteGemmOut))
+                    continue;
+                float v = value(r, c);
+                if (M == kWeightGrad && a.accumulate) v += to_f32(OT{}, *p);
+                *p = from_f32(OT{}, v);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int m0 = (i * 2 + wm) * 16;
+        const int rows = job.m_rows - m0;
+        if (rows > 0) {
+#pragma unroll
+            for (int h = 0; h < NI / 4; ++h) {
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<f32x4*>(stage + (lane & 15) * kStageRow + j * 16 +
+                                              (lane >> 4) * 4) = acc[i][h * 4 + j];
+                __builtin_amdgcn_wave_barrier();
+                const int64_t row0 = job.out_row0 + m0;
+                if constexpr (Gated) {
+                    // blocks 0 and 2 are gates, 1 and 3 their ups
+                    const int64_t col0 = job.q.first + (wn * NI + h * 4) * 8;
+                    auto gate = [&](int r, int c) {
+                        return stage[r * kStageRow + (c >> 4) * 32 + (c & 15)];
+                    };
+                    auto up = [&](int r, int c) {
+                        return stage[r * kStageRow + (c >> 4) * 32 + (c & 15) + 16];
+                    };
+                    auto both = [&](int r, int c) { return silu_mul(gate(r, c), up(r, c)); };
+                    const std::integral_constant<int, 32> cols;
+                    put(a.out, n, row0, col0, n, rows, cols, both);
+                    if (a.gate_up != nullptr) {
+                        put(a.gate_up, 2 * n, row0, col0, n, rows, cols, gate);
+                        put(static_cast<E*>(a.gate_up) + n, 2 * n, row0, col0, n, rows, cols, up);
+                    }
+                } else {
+                    const int64_t col0 = job.q.first + (wn * NI + h * 4) * 16;
+                    put(a.out, n, row0, col0, n, rows, std::integral_constant<int, 64>{},
+                        [&](int r, int c) { return stage[r * kStageRow + c]; });
+                }
+            }
+        }
+    }
+}
+
+// One tile, whose first loads are under way (Loaders::start).  `advance` sets off
+// the next tile's, between the sums and the stores.
 template <typename T, Mode M, bool Gated, int MI, typename F>
 __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, uint8_t* lds,
                                          Loaders<T, M, Gated>& loads, F&& advance) {
     using S = Tiles<T, M, Gated>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave & 1, wn = wave >> 1;
-    f32x4 acc[MI][4];
+    f32x4 acc[MI][NI];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int64_t steps = (job.len + S::kStep - 1) / S::kStep;
-    const bool aligned = a.aligned || is_fp8<T>();
+    const int64_t whole = job.len / S::kStep;
+    constexpr int kLoads = Loaders<T, M, Gated>::m_loads(MI) + 8;
     Fragments<S::kP, 2> fp;
     Fragments<S::kQ, 1> fq;
     fp.init(lds, wm, is_fp8<T>());
-    fq.init(lds + 2 * kTileBytes, wn * 4, is_fp8<T>());
-    // The products of one step from its tiles; Load: with the loads of step
-    // s + 1 (a whole one) in between.
-    auto multiply = [&](int64_t s, auto load) {
-        constexpr bool kLoad = decltype(load)::value;
-        if constexpr (is_fp8<T>()) {
-            if (kLoad) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) loads.template piece<true, MI>(job, lds, s + 1, i);
-            }
+    fq.init(lds + 2 * kTileBytes, wn * NI, is_fp8<T>());
+    auto other_tile = [&](int64_t s) {                  // from the tiles of step s to the others
+        const int bytes = (s & 1) ? -kTileBytes : kTileBytes;
+        fp.move(bytes);
+        fq.move(bytes);
+    };
+    if constexpr (is_fp8<T>()) {
+        const int64_t kb = job.len / 128;
+        for (int64_t s = 0; s < steps; ++s) {
+            wait_for_loads();
+            __syncthreads();                            // step s is there, step s - 1 is read
+            if (s + 1 < steps) loads.step(job, lds, s + 1);
             // one step is one scale block: its product, unscaled, then a
             // float32 multiply-add with both scales
-            float sq[Gated ? 4 : 1];
-            const int64_t kb = job.len / 128;
+            float sq[Gated ? NI : 1];
 #pragma unroll
-            for (int h = 0; h < (Gated ? 4 : 1); ++h) {
-                const int32_t row = tile_row<Gated>(job.q, wn * 64 + h * 16);
+            for (int h = 0; h < (Gated ? NI : 1); ++h) {
+                const int32_t row = tile_row<Gated>(job.q, (wn * NI + h) * 16);
                 const float* p = job.q_scales + (int64_t)(row >> 7) * kb + s;
                 sq[h] = MX_CAN_LOAD(p, 4, kSiteGemmScale) ? *p : 0.0f;
             }
-            i32x8 q[4];
+            i32x8 q[NI];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = fq.get_fp8(j);
+            for (int j = 0; j < NI; ++j) q[j] = fq.get_fp8(j);
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 const int32_t m = (i * 2 + wm) * 16 + (lane & 15);
@@ -355,110 +468,113 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                 const float sp = MX_CAN_LOAD(ps, 4, kSiteGemmScale) ? *ps : 0.0f;
                 const i32x8 p = fp.get_fp8(i);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < NI; ++j) {
                     const f32x4 part = mfma_fp8(q[j], p, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
                     const float sc = sp * sq[Gated ? j : 0];
 #pragma unroll
                     for (int d = 0; d < 4; ++d) acc[i][j][d] = fmaf(part[d], sc, acc[i][j][d]);
                 }
             }
-        } else {
-            // 2 MI turns of one m fragment and four matrix instructions: the
-            // fragment two turns ahead, the n fragments of the second half and
-            // the next step's loads are issued in between, in this order.
-            u32x4 q[2][4], p[3];
+            other_tile(s);
+        }
+    } else {
+        // A step is 2 MI turns of one m fragment and eight matrix instructions.
+        // Fragments are read three turns ahead, those of the next step's first
+        // turns in the last three; so the barrier between two steps stands
+        // before these, and the matrix instructions run across it.  The loads
+        // of a tile begin when the barrier frees its memory, a few per turn,
+        // and have a whole step to arrive.
+        constexpr int kTurns = 2 * MI, kFree = kTurns - 3;
+        constexpr int kPerTurn = (2 * kLoads + kTurns - 1) / kTurns;
+        constexpr int kSecond = MI < kFree ? MI : kFree;  // turns that read the second half of q
+        u32x4 q[2][NI], p[4];
+        // turns after kFree that still read the first half of q
+        constexpr int kFirst = MI > kFree ? MI - kFree : 0;
+        auto first_fragments = [&](int t) {             // of the next step, in turn kFree + t
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[0][j] = fq.get(j, 0);
-            p[0] = fp.get(0, 0);
-            p[1] = fp.get(1 % MI, 1 / MI);
+            for (int j = 0; j < NI; ++j)
+                if (t < 0 || j * 2 / NI + kFirst == t) q[0][j] = fq.get(j, 0);
+            if (t < 0 || t == 1) p[0] = fp.get(0, 0);
+            if (t < 0 || t == 2) {
+                p[1] = fp.get(1 % MI, 1 / MI);
+                p[2] = fp.get(2 % MI, 2 / MI);
+            }
+        };
+        // Next: step s + 1 is whole and follows.  rest: of its loads, those after
+        // the first three turns' are still to be set off; more: step s + 2 is whole.
+        auto multiply = [&](int64_t s, auto next, bool rest, bool more) {
+            constexpr bool kNext = decltype(next)::value;
 #pragma unroll
-            for (int t = 0; t < 2 * MI; ++t) {
-                if (t + 2 < 2 * MI) p[(t + 2) % 3] = fp.get((t + 2) % MI, (t + 2) / MI);
-                if (t < MI) {
+            for (int t = 0; t < kTurns; ++t) {
+                if (t < kFree) p[(t + 3) & 3] = fp.get((t + 3) % MI, (t + 3) / MI);
+                if (t < kSecond) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j * MI / 4 == t) q[1][j] = fq.get(j, 1);
+                    for (int j = 0; j < NI; ++j)
+                        if (j * kSecond / NI == t) q[1][j] = fq.get(j, 1);
                 }
-                if (kLoad) {
+                if (kNext && t == kFree) {
+                    wait_for_loads();
+                    __syncthreads();                    // step s + 1 is there, step s is read
+                    other_tile(s);
+                    if (rest) loads.next();
+                }
+                if (kNext && t >= kFree) first_fragments(t - kFree);
+                if (kNext && (t < kFree ? rest : more)) {
+                    const int turn = t < kFree ? t + 3 : t - kFree;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i * MI / 8 == t) loads.template piece<true, MI>(job, lds, s + 1, i);
+                    for (int i = turn * kPerTurn; i < (turn + 1) * kPerTurn; ++i)
+                        if (i < kLoads)
+                            loads.template piece<true>(job, lds, t < kFree ? s + 1 : s + 2, i,
+                                                       kLoads - 8);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[t % MI][j] = mfma_16(T{}, q[t / MI][j], p[t % 3], acc[t % MI][j]);
+                for (int j = 0; j < NI; ++j)
+                    acc[t % MI][j] = mfma_16(T{}, q[t / MI][j], p[t & 3], acc[t % MI][j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        }
-        if (kLoad) loads.next();
-        if (aligned) {
-            const int other = (s & 1) ? -kTileBytes : kTileBytes;
-            fp.move(other);
-            fq.move(other);
-        }
-    };
-    if (aligned) {
-        const int64_t whole = job.len / S::kStep;
-        int64_t s = 0;
-        for (; s + 1 < whole; ++s) {
-            wait_for_loads();
-            __syncthreads();                            // step s is there, step s - 1 is read
-            multiply(s, std::true_type{});
-        }
-        for (; s < steps; ++s) {                        // the last whole step and a partial one
+        };
+        auto tail = [&]() {                             // zeros past the end of the last step
+            const int64_t s = whole;
+            zero_tail<S::kP>(lds + (s & 1) * kTileBytes, (int)(job.len - s * S::kStep));
+            zero_tail<S::kQ>(lds + (2 + (s & 1)) * kTileBytes, (int)(job.len - s * S::kStep));
+            __syncthreads();
+        };
+        if (a.aligned && steps > 0) {
             wait_for_loads();
             __syncthreads();
-            if (s == whole) {
-                zero_tail<S::kP>(lds + (s & 1) * kTileBytes, (int)(job.len - s * S::kStep));
-                zero_tail<S::kQ>(lds + (2 + (s & 1)) * kTileBytes, (int)(job.len - s * S::kStep));
+            if (whole == 0) tail();
+            first_fragments(-1);
+            int64_t s = 0;
+            for (; s + 1 < whole; ++s) multiply(s, std::true_type{}, s > 0, s + 2 < whole);
+            const bool ragged = steps > whole && whole > 0;
+            if (ragged) loads.step(job, lds, whole);
+            multiply(s, std::false_type{}, false, false);
+            if (ragged) {
+                wait_for_loads();
                 __syncthreads();
+                tail();
+                other_tile(s);
+                first_fragments(-1);
+                multiply(whole, std::false_type{}, false, false);
             }
-            if (s + 1 < steps) loads.template all<MI>(job, lds, s + 1);
-            multiply(s, std::false_type{});
-        }
-    } else if constexpr (!is_fp8<T>()) {
-        for (int64_t s = 0; s < steps; ++s) {
-            __syncthreads();
-            stage_elements<S::kP, false>(job.p, lds, s, job.len);
-            stage_elements<S::kQ, Gated>(job.q, lds + 2 * kTileBytes, s, job.len);
-            __syncthreads();
-            multiply(0, std::false_type{});
+        } else {
+            for (int64_t s = 0; s < steps; ++s) {
+                __syncthreads();
+                stage_elements<S::kP, false>(job.p, lds, s, job.len);
+                stage_elements<S::kQ, Gated>(job.q, lds + 2 * kTileBytes, s, job.len);
+                __syncthreads();
+                first_fragments(-1);
+                multiply(0, std::false_type{}, false, false);
+            }
         }
     }
     __syncthreads();                                    // the tiles are read
     advance();
-    // Lane l holds columns 4 (l >> 4) .. + 4 of row l & 15 of each 16 x 16 block.
-    const int64_t n = a.out_cols;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int32_t m = (i * 2 + wm) * 16 + (lane & 15);
-        if (m >= job.m_rows) continue;
-        const int64_t row = job.out_row0 + m;
-        if constexpr (Gated) {
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const int64_t col = job.q.first + wn * 32 + (j / 2) * 16 + (lane >> 4) * 4;
-                f32x4 v;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) v[d] = silu_mul(acc[i][j][d], acc[i][j + 1][d]);
-                store4(a.out, a.out_dtype, a.vector_store, row * n, col, n, v, false);
-                if (a.gate_up != nullptr) {
-                    store4(a.gate_up, a.out_dtype, a.vector_store, row * 2 * n, col, n, acc[i][j],
-                           false);
-                    store4(a.gate_up, a.out_dtype, a.vector_store, row * 2 * n + n, col, n,
-                           acc[i][j + 1], false);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t col = job.q.first + wn * 64 + j * 16 + (lane >> 4) * 4;
-                store4(a.out, a.out_dtype, a.vector_store, row * n, col, n, acc[i][j],
-                       M == kWeightGrad && a.accumulate);
-            }
-        }
-    }
+    float* stage = reinterpret_cast<float*>(lds + 4 * kTileBytes) + wave * 16 * kStageRow;
+    if (a.out_dtype == 2) store_tile<BF16, M, Gated, MI>(a, job, acc, stage, wm, wn);
+    else if (a.out_dtype == 1) store_tile<F16, M, Gated, MI>(a, job, acc, stage, wm, wn);
+    else store_tile<F32, M, Gated, MI>(a, job, acc, stage, wm, wn);
 }
 
 __device__ __forceinline__ int32_t m_tiles(int32_t rows) { return (rows + kTileM - 1) / kTileM; }
@@ -466,10 +582,10 @@ __device__ __forceinline__ int32_t m_tiles(int32_t rows) { return (rows + kTileM
 // Forward and row-gradient products: a persistent grid walks the tiles of all
 // segments, whose number only the device knows.
 template <typename T, Mode M, bool Gated>
-__global__ __launch_bounds__(kThreads, 2) void gemm_rows_kernel(GemmArgs a) {
-    __shared__ __align__(16) uint8_t lds[4 * kTileBytes];
+__global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
+    __shared__ __align__(16) uint8_t lds[4 * kTileBytes + kStageBytes];
     __shared__ int32_t first_tile[kMaxExperts + 1];
-    __shared__ int32_t wave_total[kThreads / kWave];
+    __shared__ int32_t wave_total[kWaves];
     count_row_tiles<kThreads>(a, first_tile, wave_total, m_tiles);
     const int32_t cols_per_tile = Gated ? kTileN / 2 : kTileN;
     const int32_t n_tiles = (int32_t)((a.out_cols + cols_per_tile - 1) / cols_per_tile);
@@ -535,8 +651,8 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_rows_kernel(GemmArgs a) {
 // Weight gradients: E x (n tiles x k tiles) output tiles, each over the rows
 // of its expert's segment.
 template <typename T>
-__global__ __launch_bounds__(kThreads, 2) void gemm_weight_grad_kernel(GemmArgs a) {
-    __shared__ __align__(16) uint8_t lds[4 * kTileBytes];
+__global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs a) {
+    __shared__ __align__(16) uint8_t lds[4 * kTileBytes + kStageBytes];
     const int32_t mt = (int32_t)((a.out_rows + kTileM - 1) / kTileM);
     const int32_t nt = (int32_t)((a.out_cols + kTileN - 1) / kTileN);
     const int32_t tiles = mt * nt;

@@ -74,41 +74,6 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g / (1.0f + __expf(-g)) * u;
 }
 
-// Four neighbouring columns of an output row; `row`: element offset of the row,
-// `cols`: columns there are.  `add`: to what the output holds.
-template <typename T>
-__device__ __forceinline__ void store4_as(void* out, bool vec, int64_t row, int64_t col,
-                                          int64_t cols, f32x4 v, bool add) {
-    using E = typename T::storage;
-    E* p = static_cast<E*>(out) + row + col;
-    struct alignas(4 * sizeof(E)) Four { E e[4]; };
-    if (vec) {
-        if (col >= cols || !MX_CAN_STORE(p, sizeof(Four), kSiteGemmOut)) return;
-        Four f;
-        if (add) {
-            f = *reinterpret_cast<const Four*>(p);
-#pragma unroll
-            for (int d = 0; d < 4; ++d) v[d] += to_f32(T{}, f.e[d]);
-        }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) f.e[d] = from_f32(T{}, v[d]);
-        *reinterpret_cast<Four*>(p) = f;
-        return;
-    }
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        if (col + d >= cols || !MX_CAN_STORE(p + d, sizeof(E), kSiteGemmOut)) continue;
-        p[d] = from_f32(T{}, add ? v[d] + to_f32(T{}, p[d]) : v[d]);
-    }
-}
-
-__device__ __forceinline__ void store4(void* out, int dtype, bool vec, int64_t row, int64_t col,
-                                       int64_t cols, f32x4 v, bool add) {
-    if (dtype == 2) store4_as<BF16>(out, vec, row, col, cols, v, add);
-    else if (dtype == 1) store4_as<F16>(out, vec, row, col, cols, v, add);
-    else store4_as<F32>(out, vec, row, col, cols, v, add);
-}
-
 __device__ __forceinline__ void store1(void* out, int dtype, int64_t at, float v) {
     if (dtype == 0) {
         float* p = static_cast<float*>(out) + at;

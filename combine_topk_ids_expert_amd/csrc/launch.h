@@ -108,7 +108,7 @@ struct GemmArgs {
     bool transposed;          // w is [E][len][out_cols]
     bool accumulate;          // weight gradient: add to out
     bool aligned;             // rows of x and w are 16-byte aligned
-    bool vector_store;        // rows of out (and gate_up) take 4-element stores
+    bool vector_store;        // rows of out (and gate_up) take 16-byte stores
 };
 
 hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t stream);
