@@ -337,43 +337,54 @@ __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job
                                            int wn) {
     using E = typename OT::storage;
     constexpr int kChunk = 16 / (int)sizeof(E);         // elements of a 16-byte store
-    struct alignas(16) Chunk { E e[kChunk]; };
     const int lane = threadIdx.x & 63;
     const int64_t n = a.out_cols;
-    // 16 rows x `cols` columns from stage columns at(0 .. cols) to row0, col0
+    // 16 rows (of which `rows` exist) x kCols staged columns to row0, col0 of a
+    // matrix `width` wide whose columns end at `limit`
     auto put = [&](void* base, int64_t width, int64_t row0, int64_t col0, int64_t limit, int rows,
                    auto cols, auto value) {
         constexpr int kCols = decltype(cols)::value;
-        if (a.vector_store) {
-            const int r = lane >> 2;
-            E* p = static_cast<E*>(base) + (row0 + r) * width + col0;
+        constexpr int kPerRow = kCols / kChunk, kStores = 16 * kPerRow / kWave;
+        E* const corner = static_cast<E*>(base) + row0 * width + col0;
+        if (a.vector_store && col0 + kCols <= limit) {
+            // neighbouring lanes write neighbouring 16 bytes of a row
+            const __amdgpu_buffer_rsrc_t rs =
+                __builtin_amdgcn_make_buffer_rsrc(corner, (short)0, -1, 0x00020000);
+            const int r0 = lane / kPerRow, c = lane % kPerRow * kChunk;
+            const uint32_t voffset = (uint32_t)(r0 * width + c) * (uint32_t)sizeof(E);
+            const uint32_t down = kWave / kPerRow * (uint32_t)width * (uint32_t)sizeof(E);
+            union Store { u32x4 raw; E e[kChunk]; };
+            Store v[kStores];
+            const bool add = M == kWeightGrad && a.accumulate;
+            if (add) {
 #pragma unroll
-            for (int i = 0; i < kCols / 4; i += kChunk) {
-                const int c = (lane & 3) * (kCols / 4) + i;
-                if (r >= rows || col0 + c >= limit || !MX_CAN_STORE(p + c, 16, kSiteGemmOut))
-                    continue;
-                Chunk v;
-                if (M == kWeightGrad && a.accumulate) {
-                    v = *reinterpret_cast<const Chunk*>(p + c);
+                for (int k = 0; k < kStores; ++k)
+                    if (r0 + k * (kWave / kPerRow) < rows)
+                        v[k].raw = __builtin_amdgcn_raw_buffer_load_b128(rs, voffset, k * down, 0);
+            }
 #pragma unroll
-                    for (int d = 0; d < kChunk; ++d)
-                        v.e[d] = from_f32(OT{}, value(r, c + d) + to_f32(OT{}, v.e[d]));
-                } else {
+            for (int k = 0; k < kStores; ++k)
 #pragma unroll
-                    for (int d = 0; d < kChunk; ++d) v.e[d] = from_f32(OT{}, value(r, c + d));
+                for (int d = 0; d < kChunk; ++d) {
+                    const float f = value(r0 + k * (kWave / kPerRow), c + d);
+                    v[k].e[d] = from_f32(OT{}, add ? f + to_f32(OT{}, v[k].e[d]) : f);
                 }
-                *reinterpret_cast<Chunk*>(p + c) = v;
+#pragma unroll
+            for (int k = 0; k < kStores; ++k) {
+                const int r = r0 + k * (kWave / kPerRow);
+                if (r < rows && MX_CAN_STORE(corner + r * width + c, 16, kSiteGemmOut))
+                    __builtin_amdgcn_raw_buffer_store_b128(v[k].raw, rs, voffset, k * down, 0);
             }
         } else {
+            const int here = rows < 16 ? rows : 16;
 #pragma unroll 1
-            for (int at = lane; at < 16 * kCols; at += kWave) {
+            for (int at = lane; at < here * kCols; at += kWave) {
                 const int r = at / kCols, c = at % kCols;
-                E* p = static_cast<E*>(base) + (row0 + r) * width + col0 + c;
-                if (r >= rows || col0 + c >= limit || !MX_CAN_STORE(p, sizeof(E), kSiteGemmOut))
-                    continue;
-                float v = value(r, c);
-                if (M == kWeightGrad && a.accumulate) v += to_f32(OT{}, *p);
-                *p = from_f32(OT{}, v);
+                E* p = corner + r * width + c;
+                if (col0 + c >= limit || !MX_CAN_STORE(p, sizeof(E), kSiteGemmOut)) continue;
+                float f = value(r, c);
+                if (M == kWeightGrad && a.accumulate) f += to_f32(OT{}, *p);
+                *p = from_f32(OT{}, f);
             }
         }
     };
