@@ -18,6 +18,8 @@
 //   softmax over all:       dl_e = scale p_e ([e chosen] g_e - sum_i p_i g_i)
 //   sigmoid, renormalized:  ds_j = scale (g_j - sum_i w_i g_i) / sum s
 //   sigmoid:                ds_j = scale g_j;   dl = ds s (1 - s)
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 
@@ -56,12 +58,12 @@ __device__ __forceinline__ float exp_below(float x, float m) {
     return x == m ? 1.0f : expf(x - m);
 }
 
-// Lane l holds experts l, l + 64, ...: PER of them.
+// One token with a whole wave, one pick after the other: the form that takes
+// any k and any number of equal keys.  Lane l holds experts l, l + 64, ...: PER
+// of them.
 template <typename T, int PER>
-__global__ __launch_bounds__(kThreads) void topk_gating_kernel(GatingArgs a) {
+__device__ __forceinline__ void gate_token(const GatingArgs& a, int64_t t) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * kTokens + (threadIdx.x >> 6);
-    if (t >= a.num_tokens) return;
     const int E = a.num_experts;
     float x[PER];
     double key[PER];
@@ -134,6 +136,222 @@ __global__ __launch_bounds__(kThreads) void topk_gating_kernel(GatingArgs a) {
         float* w = a.weights + t * a.topk + lane;
         if (MX_CAN_STORE(id, 4, kSiteTopkOut)) *id = my_id;
         if (MX_CAN_STORE(w, 4, kSiteTopkOut)) *w = total > 0.0f ? a.scale * (p / total) : 0.0f;
+    }
+}
+
+template <typename T, int PER>
+__global__ __launch_bounds__(kThreads) void topk_gating_wave_kernel(GatingArgs a) {
+    const int64_t t = (int64_t)blockIdx.x * kTokens + (threadIdx.x >> 6);
+    if (t < a.num_tokens) gate_token<T, PER>(a, t);
+}
+
+// ---- four tokens to a wave, for few picks ------------------------------------
+// 16 lanes hold a token's logits, 4 NC each.  The k-th largest of their 16
+// maxima is a bound that at least k experts reach, and few more do: about 16 (1/16
+// + ... + 1/(17 - k)), 13 of 288 for k = 8.  Those are put into a list in LDS,
+// and each counts the list's larger keys, which is its place.  So no pick waits
+// for the one before, and with a bias only the listed keys are computed in
+// float64.  A list of more than kList goes through gate_token.
+constexpr int kRowTopk = 12;
+constexpr int kList = 32;
+
+template <int Ctrl>
+__device__ __forceinline__ float dpp_f(float v) {
+    return __int_as_float(dpp<Ctrl>(__float_as_int(v)));
+}
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, dpp_f<0xb1>(v));
+    v = fmaxf(v, dpp_f<0x4e>(v));
+    v = fmaxf(v, dpp_f<0x141>(v));
+    return fmaxf(v, dpp_f<0x140>(v));
+}
+__device__ __forceinline__ float row_min(float v) { return -row_max(-v); }
+__device__ __forceinline__ float row_sum(float v) {
+    v += dpp_f<0xb1>(v);
+    v += dpp_f<0x4e>(v);
+    v += dpp_f<0x141>(v);
+    return v + dpp_f<0x140>(v);
+}
+// How many of a row's 16 values are larger than the lane's.
+template <int N = 15>
+__device__ __forceinline__ int row_larger(float v) {
+    const int here = dpp_f<0x120 + N>(v) > v ? 1 : 0;       // row_ror:N
+    if constexpr (N > 1) return here + row_larger<N - 1>(v);
+    return here;
+}
+// Sum of the lanes below in the row.
+__device__ __forceinline__ int row_before(int v) {
+    int s = v;
+    s += dpp<0x111>(s);
+    s += dpp<0x112>(s);
+    s += dpp<0x114>(s);
+    s += dpp<0x118>(s);
+    return s - v;
+}
+
+template <typename T, int NC>
+__global__ __launch_bounds__(kThreads, NC <= 5 ? 4 : NC <= 8 ? 3 : 2) void topk_gating_kernel(
+    GatingArgs a, bool vec, bool vec_bias) {
+    struct Entry { float x; int32_t id; };
+    __shared__ Entry list[kThreads / 16][kList];
+    __shared__ double keys[kThreads / 16][kList];
+    const int lane = threadIdx.x & 63, l = lane & 15, row = threadIdx.x >> 4;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / 16) + row;
+    const bool live = t < a.num_tokens;
+    const int E = a.num_experts;
+    using S = typename T::storage;
+    struct alignas(4 * sizeof(S)) Four { S v[4]; };
+    // Keys in float32 of experts (16 c + l) 4 + i: the logits, or with a bias
+    // values within 2^-21 max(1, |key|) of the float64 ones (the exponential's and
+    // the quotient's few roundings).
+    float key[NC][4], mine = -kInf, all_sum = 0.0f;
+    const S* logits = static_cast<const S*>(a.logits) + t * E;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int e = (c * 16 + l) * 4;
+        if (vec && live && e < E && MX_CAN_LOAD(logits + e, sizeof(Four), kSiteTopkLoad)) {
+            const Four f = *reinterpret_cast<const Four*>(logits + e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) key[c][i] = to_f32(T{}, f.v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                key[c][i] = !vec && live && e + i < E ? logit<T>(a.logits, t * E + e + i) : -kInf;
+        }
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int e = (c * 16 + l) * 4;
+            struct alignas(16) Four32 { float v[4]; };
+            Four32 b{};
+            if (vec_bias) {
+                if (e < E && MX_CAN_LOAD(a.bias + e, 16, kSiteTopkLoad))
+                    b = *reinterpret_cast<const Four32*>(a.bias + e);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (e + i < E && MX_CAN_LOAD(a.bias + e + i, 4, kSiteTopkLoad))
+                        b.v[i] = a.bias[e + i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = key[c][i], k = __builtin_amdgcn_rcpf(1.0f + __expf(-x)) + b.v[i];
+                key[c][i] = x > -kInf ? k : -kInf;
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            key[c][i] = fmaxf(key[c][i], -kInf);               // NaN becomes -inf
+            mine = fmaxf(mine, key[c][i]);
+        }
+    const float most = row_max(mine);
+    if (!a.sigmoid && !a.renormalize) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (key[c][i] > -kInf) all_sum += exp_below(key[c][i], most);
+        all_sum = row_sum(all_sum);
+    }
+    float bound = row_min(row_larger(mine) < a.topk ? mine : kInf);
+    if (a.bias != nullptr && bound > -kInf && bound < kInf)
+        bound -= 0x1p-19f * fmaxf(1.0f, fabsf(bound));      // twice the keys' error, and more
+    bound = fmaxf(bound, -3.402823466e38f);                 // of finite keys the lowest
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += key[c][i] >= bound ? 1 : 0;
+    int at = row_before(n);
+    const int count = __builtin_amdgcn_ds_bpermute((lane | 15) * 4, at + n);
+    if (__ballot(count > kList) != 0) {
+        const int64_t t0 = t - (lane >> 4);
+        for (int r = 0; r < 4; ++r)
+            if (t0 + r < a.num_tokens) gate_token<T, NC>(a, t0 + r);
+        return;
+    }
+    // unused entries lose against every other
+    list[row][l] = list[row][l + 16] = Entry{-kInf, 0x7fffffff};
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (key[c][i] >= bound)
+                list[row][at++] = Entry{key[c][i], (c * 16 + l) * 4 + i};
+    // lane l takes entries l and l + 16
+    const bool two = __ballot(count > 16) != 0;
+    Entry my[2] = {list[row][l], list[row][l + 16]};
+    int rank[2] = {0, 0};
+    if (a.bias != nullptr) {
+        double exact[2] = {-(double)kInf, -(double)kInf};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h == 1 && !two) break;
+            if (l + 16 * h < count) {
+                const float b = MX_CAN_LOAD(a.bias + my[h].id, 4, kSiteTopkLoad)
+                                    ? a.bias[my[h].id] : 0.0f;
+                my[h].x = logit<T>(a.logits, t * E + my[h].id);
+                exact[h] = 1.0 / (1.0 + exp(-(double)my[h].x)) + (double)b;
+            }
+            keys[row][l + 16 * h] = exact[h];
+        }
+        auto count_larger = [&](int h, int first) {
+#pragma unroll
+            for (int j = first; j < first + 16; ++j) {
+                const double k = keys[row][j];
+                rank[h] += k > exact[h] || (k == exact[h] && list[row][j].id < my[h].id) ? 1 : 0;
+            }
+        };
+        count_larger(0, 0);
+        if (two) {
+            count_larger(0, 16);
+            count_larger(1, 0);
+            count_larger(1, 16);
+        }
+    } else {
+        auto count_larger = [&](int h, int first) {
+#pragma unroll
+            for (int j = first; j < first + 16; ++j) {
+                const Entry o = list[row][j];
+                rank[h] += o.x > my[h].x || (o.x == my[h].x && o.id < my[h].id) ? 1 : 0;
+            }
+        };
+        count_larger(0, 0);
+        if (two) {
+            count_larger(0, 16);
+            count_larger(1, 0);
+            count_larger(1, 16);
+        }
+    }
+    float p[2], total = 0.0f;
+    bool chosen[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        chosen[h] = l + 16 * h < count && rank[h] < a.topk;
+        p[h] = !chosen[h] ? 0.0f : a.sigmoid ? sigmoid(my[h].x) : exp_below(my[h].x, most);
+        total += p[h];
+    }
+    total = row_sum(total);
+    if (!a.renormalize) total = a.sigmoid ? 1.0f : all_sum;
+    if (!live) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (chosen[h]) {
+            int32_t* id = a.ids + t * a.topk + rank[h];
+            float* w = a.weights + t * a.topk + rank[h];
+            if (MX_CAN_STORE(id, 4, kSiteTopkOut)) *id = my[h].id;
+            if (MX_CAN_STORE(w, 4, kSiteTopkOut))
+                *w = total > 0.0f ? a.scale * (p[h] / total) : 0.0f;
+        }
+    if (l >= count && l < a.topk) {
+        int32_t* id = a.ids + t * a.topk + l;
+        float* w = a.weights + t * a.topk + l;
+        if (MX_CAN_STORE(id, 4, kSiteTopkOut)) *id = -1;
+        if (MX_CAN_STORE(w, 4, kSiteTopkOut)) *w = 0.0f;
     }
 }
 
@@ -216,47 +434,77 @@ __global__ __launch_bounds__(kThreads) void topk_gating_backward_kernel(GatingAr
     }
 }
 
-template <typename T, bool Backward>
-hipError_t start(const GatingArgs& a, hipStream_t stream) {
-    auto go = [&](auto kernel) {
-        for (int64_t t0 = 0; t0 < a.num_tokens; t0 += kTokensPerLaunch) {
-            GatingArgs b = a;
-            b.num_tokens = a.num_tokens - t0 < kTokensPerLaunch ? a.num_tokens - t0 : kTokensPerLaunch;
-            const int64_t row = t0 * a.num_experts * (int64_t)sizeof(typename T::storage);
-            b.logits = static_cast<const uint8_t*>(a.logits) + row;
-            if (Backward) b.grad_logits = static_cast<uint8_t*>(a.grad_logits) + row;
-            b.ids = a.ids + t0 * a.topk;
-            b.weights = a.weights + t0 * a.topk;
-            const dim3 grid((unsigned)((b.num_tokens + kTokens - 1) / kTokens));
-            launch_kernel(kernel, grid, dim3(kThreads), 0, stream, nullptr, nullptr, b);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-        }
-        return hipSuccess;
-    };
-    const int per = (a.num_experts + kWave - 1) / kWave;
-#define MX_PER(n) \
-    if (per <= n) return Backward ? go(topk_gating_backward_kernel<T, n>) : go(topk_gating_kernel<T, n>);
-    MX_PER(1) MX_PER(2) MX_PER(4) MX_PER(5) MX_PER(8) MX_PER(16)
-#undef MX_PER
-    return hipErrorInvalidValue;
+// go(arguments, workgroups) for batches of tokens, `per_group` to a workgroup.
+template <typename T, typename F>
+hipError_t for_token_batches(const GatingArgs& a, int per_group, F&& go) {
+    for (int64_t t0 = 0; t0 < a.num_tokens; t0 += kTokensPerLaunch) {
+        GatingArgs b = a;
+        b.num_tokens = a.num_tokens - t0 < kTokensPerLaunch ? a.num_tokens - t0 : kTokensPerLaunch;
+        const int64_t row = t0 * a.num_experts * (int64_t)sizeof(typename T::storage);
+        b.logits = static_cast<const uint8_t*>(a.logits) + row;
+        if (a.grad_logits != nullptr) b.grad_logits = static_cast<uint8_t*>(a.grad_logits) + row;
+        b.ids = a.ids + t0 * a.topk;
+        b.weights = a.weights + t0 * a.topk;
+        go(b, dim3((unsigned)((b.num_tokens + per_group - 1) / per_group)));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
-template <bool Backward>
+// The kernel for lanes that hold n = 1, 2, ... 64ths of the experts.
+#define MX_PER_LANE(go) \
+    if (per <= 1) return go(std::integral_constant<int, 1>{}); \
+    if (per <= 2) return go(std::integral_constant<int, 2>{}); \
+    if (per <= 4) return go(std::integral_constant<int, 4>{}); \
+    if (per <= 5) return go(std::integral_constant<int, 5>{}); \
+    if (per <= 8) return go(std::integral_constant<int, 8>{}); \
+    return go(std::integral_constant<int, 16>{});
+
+template <typename T>
 hipError_t start(const GatingArgs& a, hipStream_t stream) {
-    if (a.dtype == 0) return start<F32, Backward>(a, stream);
-    if (a.dtype == 1) return start<F16, Backward>(a, stream);
-    return start<BF16, Backward>(a, stream);
+    const int per = (a.num_experts + kWave - 1) / kWave;
+    const bool rows = a.topk <= kRowTopk;
+    const bool vec = a.num_experts % 4 == 0 &&
+                     (uintptr_t)a.logits % (4 * sizeof(typename T::storage)) == 0;
+    auto go = [&](auto n) {
+        return for_token_batches<T>(a, rows ? kThreads / 16 : kTokens, [&](const GatingArgs& b,
+                                                                         dim3 grid) {
+            if (rows)
+                launch_kernel(topk_gating_kernel<T, decltype(n)::value>, grid, dim3(kThreads), 0,
+                              stream, nullptr, nullptr, b, vec, vec && (uintptr_t)a.bias % 16 == 0);
+            else
+                launch_kernel(topk_gating_wave_kernel<T, decltype(n)::value>, grid,
+                              dim3(kThreads), 0, stream, nullptr, nullptr, b);
+        });
+    };
+    MX_PER_LANE(go)
+}
+
+template <typename T>
+hipError_t start_backward(const GatingArgs& a, hipStream_t stream) {
+    const int per = (a.num_experts + kWave - 1) / kWave;
+    auto go = [&](auto n) {
+        return for_token_batches<T>(a, kTokens, [&](const GatingArgs& b, dim3 grid) {
+            launch_kernel(topk_gating_backward_kernel<T, decltype(n)::value>, grid, dim3(kThreads),
+                          0, stream, nullptr, nullptr, b);
+        });
+    };
+    MX_PER_LANE(go)
 }
 
 }  // namespace
 
 hipError_t launch_topk_gating(const GatingArgs& a, hipStream_t stream) {
-    return start<false>(a, stream);
+    if (a.dtype == 0) return start<F32>(a, stream);
+    if (a.dtype == 1) return start<F16>(a, stream);
+    return start<BF16>(a, stream);
 }
 
 hipError_t launch_topk_gating_backward(const GatingArgs& a, hipStream_t stream) {
-    return start<true>(a, stream);
+    if (a.dtype == 0) return start_backward<F32>(a, stream);
+    if (a.dtype == 1) return start_backward<F16>(a, stream);
+    return start_backward<BF16>(a, stream);
 }
 
 }  // namespace mxmoe
