@@ -32,11 +32,13 @@ CHECKED_FLAGS = ["-DMXMOE_CHECKED=1"]
 # Routing: single-workgroup path up to 512 picks (1024 with little padding),
 # no medium path, at most 16 tiles and a quarter of the table budget; row
 # kernels: 256-thread copies, 128-thread combine chunks, 64-thread zeroing,
-# 256-thread FP8 chunks, 8 padding-fill slices.
+# 256-thread FP8 chunks, 8 padding-fill slices; expert products: fewer
+# workgroups, wide tiles only.
 ALTGRID_FLAGS = ["-DMXMOE_FUSED_MAX=1024", "-DMXMOE_FUSED_ALWAYS=512", "-DMXMOE_SPREAD_MAX=0",
                  "-DMXMOE_MAX_TILES=16", "-DMXMOE_TABLE_BUDGET=4096", "-DMXMOE_ZERO_SLICES=8",
                  "-DMXMOE_ROW_THREADS=256", "-DMXMOE_COMBINE_THREADS=128",
-                 "-DMXMOE_ZERO_THREADS=64", "-DMXMOE_QUANT_THREADS=256"]
+                 "-DMXMOE_ZERO_THREADS=64", "-DMXMOE_QUANT_THREADS=256",
+                 "-DMXMOE_GEMM_GROUPS=64", "-DMXMOE_GEMM_NARROW_ROWS=0", "-DMXMOE_SKINNY_GROUPS=128"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -24,10 +24,9 @@ namespace {
 // read 192 KiB together in place of 128, as long as their matrix instructions
 // take.
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
-constexpr int kTileM = 256, kTileN = 256;
+constexpr int kTileM = 256, kTileN = 256; // of the wide tiles
 constexpr int NI = 8;                     // 16-column blocks of a wave
 constexpr int kStepBytes = 128;           // contraction bytes of one step, a tile row in LDS
-constexpr int kTileBytes = 256 * kStepBytes;
 constexpr int kXcds = 8;
 
 enum Mode { kForward, kRowGrad, kWeightGrad };
@@ -58,9 +57,22 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t 
                  :: "v"(voffset), "s"(rs), "s"(soffset), "s"(lds) : "memory");
 }
 
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t voffset,
+                                             uint32_t soffset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 :: "v"(voffset), "s"(rs), "s"(soffset), "s"(lds) : "memory");
+}
+
 // The loads to LDS that this wave has issued are done; a barrier by itself
 // does not wait for them.
 __device__ __forceinline__ void wait_for_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// All but the `N` memory operations issued last are done.
+template <int N>
+__device__ __forceinline__ void wait_for_all_but() {
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
 
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
@@ -145,11 +157,11 @@ struct Loader {
 
 // The same for rows that are not 16-byte aligned, element by element, with
 // zeros past every end.
-template <Kind K, bool Gated>
+template <Kind K, bool Gated, int Rows>
 __device__ __forceinline__ void stage_elements(const Operand& o, uint8_t* tile, int64_t step,
                                                int64_t len) {
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < Rows * kStepBytes / 16 / kThreads; ++i) {
         const int piece = i * kThreads + threadIdx.x;       // 16 bytes of the tile
         uint32_t v[4];
 #pragma unroll
@@ -181,10 +193,10 @@ __device__ __forceinline__ void stage_elements(const Operand& o, uint8_t* tile, 
 }
 
 // Zeros at the contraction positions past `valid` (< 64) of a staged tile.
-template <Kind K>
+template <Kind K, int Rows>
 __device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < Rows * kStepBytes / 16 / kThreads; ++i) {
         const int piece = i * kThreads + threadIdx.x;
         bool past;
         if constexpr (K == kAlong) past = ((piece & 7) ^ ((piece >> 3) & 7)) * 8 >= valid;
@@ -257,12 +269,27 @@ struct Fragments {
 template <typename T>
 constexpr bool is_fp8() { return __is_same(T, FP8); }
 
-template <typename T, Mode M, bool Gated>
+// Tiles of the m and the n operand for one step make a slot of LDS.  Wide: 256
+// rows, two slots, for the matrix cores; narrow: 128 rows and three slots, two
+// steps of loads under way, for experts with so few rows that their weights'
+// bytes are the time, and for FP8, whose float32 sums are made by vector
+// instructions and so have to fit half the registers.
+template <typename T, Mode M, bool Gated, bool Wide>
 struct Tiles {
     static constexpr Kind kP = M == kWeightGrad ? kAcross : kAlong;   // m side
     static constexpr Kind kQ = M == kForward ? kAlong : kAcross;      // n side
     static constexpr int kElem = is_fp8<T>() ? 1 : 2;
     static constexpr int kStep = kStepBytes / kElem;                  // contraction per step
+    static constexpr int kRows = Wide ? kTileM : kTileM / 2;
+    static constexpr int kSlots = Wide ? 2 : 3;
+    static constexpr int kPBytes = kRows * kStepBytes, kQBytes = kTileN * kStepBytes;
+    static constexpr int kScaleBytes = is_fp8<T>() ? 768 : 0;         // 128 rows, 16 blocks
+    static constexpr int kSlot = kPBytes + kQBytes + kScaleBytes;
+    // Results pass through LDS 16 rows x kStageCols columns of a wave at a time.
+    static constexpr int kStageCols = Wide ? 64 : 32;
+    static constexpr int kStageRow = kStageCols + 4;  // floats; the rest spreads the banks
+    static constexpr int kLds = kSlots * kSlot + kWaves * 16 * kStageRow * 4;
+    static constexpr int next(int slot) { return slot + 1 == kSlots ? 0 : slot + 1; }
 };
 
 // One output tile: rows 0 .. m_rows of the m operand, columns of the n
@@ -276,46 +303,71 @@ struct TileJob {
     const float* q_scales;
 };
 
-template <typename T, Mode M, bool Gated>
+template <typename T, Mode M, bool Gated, bool Wide>
 struct Loaders {
-    using S = Tiles<T, M, Gated>;
+    using S = Tiles<T, M, Gated, Wide>;
     Loader<S::kP, false, S::kElem> p;
     Loader<S::kQ, Gated, S::kElem> q;
+    uint32_t scale_offset;        // fp8: of the lane's row (waves 0, 1) or block (wave 2)
 
     // Loads of the m operand of a tile of 32 MI rows.
     static constexpr int m_loads(int MI) { return S::kP == kAlong ? MI : 8; }
 
     // Readies the loads of a tile and, where its rows are aligned, sets off
-    // those of its first step, and of the second if both are whole (FP8: of
-    // the first).
+    // those of its first step, and of the second if both are whole.
     __device__ __forceinline__ void start(const GemmArgs& a, const TileJob& job, uint8_t* lds) {
         if (!a.aligned || job.len <= 0) return;
         p.init(job.p);
         q.init(job.q);
-        step(job, lds, 0);
-        if (!is_fp8<T>() && job.len >= 2 * S::kStep) step(job, lds, 1);
+        if constexpr (is_fp8<T>()) {
+            const uint32_t row_bytes = (uint32_t)(job.len / 128) * 4;
+            const int row = threadIdx.x & 127, block = threadIdx.x & 15;
+            scale_offset = threadIdx.x < 128
+                               ? (uint32_t)(row < job.m_rows ? row : job.m_rows - 1) * row_bytes
+                               : (uint32_t)(tile_row<Gated>(job.q, block * 16) >> 7) * row_bytes;
+        }
+        step(job, lds, 0, 0);
+        if (job.len >= 2 * S::kStep) step(job, lds, 1, 1);
     }
-    // Load i of step s: first the m operand's, then the eight of the n operand.
+    // Load i of step s into a slot: first the m operand's, then the eight of
+    // the n operand.
     template <bool Whole>
-    __device__ __forceinline__ void piece(const TileJob& job, uint8_t* lds, int64_t s, int i,
-                                          int m_loads) {
+    __device__ __forceinline__ void piece(const TileJob& job, const uint8_t* slot, int64_t s,
+                                          int i, int m_loads) {
         const int64_t valid = job.len - s * S::kStep;
-        uint8_t* tile = lds + (s & 1) * kTileBytes;
-        if (i >= m_loads) q.template piece<Whole>(job.q, tile + 2 * kTileBytes, i - m_loads, valid);
-        else p.template piece<Whole>(job.p, tile, i, valid);
+        if (i >= m_loads) q.template piece<Whole>(job.q, slot + S::kPBytes, i - m_loads, valid);
+        else p.template piece<Whole>(job.p, slot, i, valid);
     }
-    // All loads of step s, the next one.
-    __device__ __forceinline__ void step(const TileJob& job, uint8_t* lds, int64_t s) {
+    // fp8: the scales of step s, 64 per wave: of the rows, then of the blocks.
+    __device__ __forceinline__ void scales(const TileJob& job, const uint8_t* slot, int64_t s) {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        if (wave == 3) return;
+        const float* base = wave < 2 ? job.p_scales : job.q_scales;
+        const __amdgpu_buffer_rsrc_t rs =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), (short)0, -1, 0x00020000);
+        if (!MX_CAN_LOAD(reinterpret_cast<const uint8_t*>(base) + scale_offset + s * 4, 4,
+                         kSiteGemmScale))
+            return;
+        load4_to_lds(rs, scale_offset, (uint32_t)uniform((int32_t)s * 4),
+                     lds_address(slot + S::kPBytes + S::kQBytes) + wave * 256);
+    }
+    // All loads of step s, the next one, into slot number `at`.
+    __device__ __forceinline__ void step(const TileJob& job, uint8_t* lds, int64_t s, int at) {
         const bool whole = job.len - s * S::kStep >= S::kStep;
         const int rows = (job.m_rows + 63) / 64 * 64;
+        const uint8_t* slot = lds + at * S::kSlot;
+        constexpr int kM = S::kRows / 32;
+        if constexpr (is_fp8<T>()) scales(job, slot, s);
         if (whole) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i >= 8 || S::kP == kAcross || i * 32 < rows) piece<true>(job, lds, s, i, 8);
+            for (int i = 0; i < kM + 8; ++i)
+                if (i >= kM || S::kP == kAcross || i * 32 < rows)
+                    piece<true>(job, slot, s, i, kM);
         } else {
 #pragma unroll 1
-            for (int i = 0; i < 16; ++i)
-                if (i >= 8 || S::kP == kAcross || i * 32 < rows) piece<false>(job, lds, s, i, 8);
+            for (int i = 0; i < kM + 8; ++i)
+                if (i >= kM || S::kP == kAcross || i * 32 < rows)
+                    piece<false>(job, slot, s, i, kM);
         }
         next();
     }
@@ -325,18 +377,16 @@ struct Loaders {
     }
 };
 
-// Writes a tile's results.  They pass through LDS, 16 rows x 64 columns of a
-// wave at a time, so that each row is written in pieces of 64 to 256 bytes.
+// Writes a tile's results.  They pass through LDS, 16 rows x StageCols columns
+// of a wave at a time, so that each row is written in pieces of 64 to 256 bytes.
 // Lane l of a result holds columns 4 (l >> 4) .. + 4 of row l & 15 of a block.
-constexpr int kStageRow = 64 + 4;                       // floats; the rest spreads the banks
-constexpr int kStageBytes = kWaves * 16 * kStageRow * 4;
-
-template <typename OT, Mode M, bool Gated, int MI>
+template <typename OT, Mode M, bool Gated, int StageCols, int MI>
 __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job,
                                            const f32x4 (&acc)[MI][NI], float* stage, int wm,
                                            int wn) {
     using E = typename OT::storage;
     constexpr int kChunk = 16 / (int)sizeof(E);         // elements of a 16-byte store
+    constexpr int kStageRow = StageCols + 4, kBlocks = StageCols / 16;
     const int lane = threadIdx.x & 63;
     const int64_t n = a.out_cols;
     // 16 rows (of which `rows` exist) x kCols staged columns to row0, col0 of a
@@ -344,13 +394,15 @@ __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job
     auto put = [&](void* base, int64_t width, int64_t row0, int64_t col0, int64_t limit, int rows,
                    auto cols, auto value) {
         constexpr int kCols = decltype(cols)::value;
-        constexpr int kPerRow = kCols / kChunk, kStores = 16 * kPerRow / kWave;
+        constexpr int kPerRow = kCols / kChunk;             // stores of a row
+        constexpr int kStores = (16 * kPerRow + kWave - 1) / kWave;
         E* const corner = static_cast<E*>(base) + row0 * width + col0;
         if (a.vector_store && col0 + kCols <= limit) {
             // neighbouring lanes write neighbouring 16 bytes of a row
             const __amdgpu_buffer_rsrc_t rs =
                 __builtin_amdgcn_make_buffer_rsrc(corner, (short)0, -1, 0x00020000);
-            const int r0 = lane / kPerRow, c = lane % kPerRow * kChunk;
+            const int r0 = lane / kPerRow < 16 ? lane / kPerRow : 15;
+            const int c = lane % kPerRow * kChunk;
             const uint32_t voffset = (uint32_t)(r0 * width + c) * (uint32_t)sizeof(E);
             const uint32_t down = kWave / kPerRow * (uint32_t)width * (uint32_t)sizeof(E);
             union Store { u32x4 raw; E e[kChunk]; };
@@ -372,7 +424,7 @@ __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job
 #pragma unroll
             for (int k = 0; k < kStores; ++k) {
                 const int r = r0 + k * (kWave / kPerRow);
-                if (r < rows && MX_CAN_STORE(corner + r * width + c, 16, kSiteGemmOut))
+                if (r < rows && lane / kPerRow < 16 && MX_CAN_STORE(corner + r * width + c, 16, kSiteGemmOut))
                     __builtin_amdgcn_raw_buffer_store_b128(v[k].raw, rs, voffset, k * down, 0);
             }
         } else {
@@ -394,17 +446,17 @@ __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job
         const int rows = job.m_rows - m0;
         if (rows > 0) {
 #pragma unroll
-            for (int h = 0; h < NI / 4; ++h) {
+            for (int h = 0; h < NI / kBlocks; ++h) {
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < kBlocks; ++j)
                     *reinterpret_cast<f32x4*>(stage + (lane & 15) * kStageRow + j * 16 +
-                                              (lane >> 4) * 4) = acc[i][h * 4 + j];
+                                              (lane >> 4) * 4) = acc[i][h * kBlocks + j];
                 __builtin_amdgcn_wave_barrier();
                 const int64_t row0 = job.out_row0 + m0;
                 if constexpr (Gated) {
                     // blocks 0 and 2 are gates, 1 and 3 their ups
-                    const int64_t col0 = job.q.first + (wn * NI + h * 4) * 8;
+                    const int64_t col0 = job.q.first + (wn * NI + h * kBlocks) * 8;
                     auto gate = [&](int r, int c) {
                         return stage[r * kStageRow + (c >> 4) * 32 + (c & 15)];
                     };
@@ -412,15 +464,15 @@ __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job
                         return stage[r * kStageRow + (c >> 4) * 32 + (c & 15) + 16];
                     };
                     auto both = [&](int r, int c) { return silu_mul(gate(r, c), up(r, c)); };
-                    const std::integral_constant<int, 32> cols;
+                    const std::integral_constant<int, StageCols / 2> cols;
                     put(a.out, n, row0, col0, n, rows, cols, both);
                     if (a.gate_up != nullptr) {
                         put(a.gate_up, 2 * n, row0, col0, n, rows, cols, gate);
                         put(static_cast<E*>(a.gate_up) + n, 2 * n, row0, col0, n, rows, cols, up);
                     }
                 } else {
-                    const int64_t col0 = job.q.first + (wn * NI + h * 4) * 16;
-                    put(a.out, n, row0, col0, n, rows, std::integral_constant<int, 64>{},
+                    const int64_t col0 = job.q.first + (wn * NI + h * kBlocks) * 16;
+                    put(a.out, n, row0, col0, n, rows, std::integral_constant<int, StageCols>{},
                         [&](int r, int c) { return stage[r * kStageRow + c]; });
                 }
             }
@@ -430,10 +482,10 @@ __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job
 
 // One tile, whose first loads are under way (Loaders::start).  `advance` sets off
 // the next tile's, between the sums and the stores.
-template <typename T, Mode M, bool Gated, int MI, typename F>
+template <typename T, Mode M, bool Gated, bool Wide, int MI, typename F>
 __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, uint8_t* lds,
-                                         Loaders<T, M, Gated>& loads, F&& advance) {
-    using S = Tiles<T, M, Gated>;
+                                         Loaders<T, M, Gated, Wide>& loads, F&& advance) {
+    using S = Tiles<T, M, Gated, Wide>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave & 1, wn = wave >> 1;
     f32x4 acc[MI][NI];
@@ -443,60 +495,117 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
         for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int64_t steps = (job.len + S::kStep - 1) / S::kStep;
     const int64_t whole = job.len / S::kStep;
-    constexpr int kLoads = Loaders<T, M, Gated>::m_loads(MI) + 8;
+    constexpr int kLoads = Loaders<T, M, Gated, Wide>::m_loads(MI) + 8;
     Fragments<S::kP, 2> fp;
     Fragments<S::kQ, 1> fq;
     fp.init(lds, wm, is_fp8<T>());
-    fq.init(lds + 2 * kTileBytes, wn * NI, is_fp8<T>());
-    auto other_tile = [&](int64_t s) {                  // from the tiles of step s to the others
-        const int bytes = (s & 1) ? -kTileBytes : kTileBytes;
+    fq.init(lds + S::kPBytes, wn * NI, is_fp8<T>());
+    int at = 0;                                         // the slot of the step at hand
+    auto next_slot = [&]() {
+        const int bytes = at + 1 == S::kSlots ? -at * S::kSlot : S::kSlot;
         fp.move(bytes);
         fq.move(bytes);
+        at = S::next(at);
+    };
+    // Narrow tiles: loads first .. last of step s + 2.
+    auto load_ahead = [&](int64_t s, int first, int last) {
+        const uint8_t* slot = lds + S::next(S::next(at)) * S::kSlot;
+#pragma unroll
+        for (int i = first; i < last; ++i)
+            if (i < kLoads) loads.template piece<true>(job, slot, s + 2, i, kLoads - 8);
     };
     if constexpr (is_fp8<T>()) {
-        const int64_t kb = job.len / 128;
-        for (int64_t s = 0; s < steps; ++s) {
-            wait_for_loads();
-            __syncthreads();                            // step s is there, step s - 1 is read
-            if (s + 1 < steps) loads.step(job, lds, s + 1);
-            // one step is one scale block: its product, unscaled, then a
-            // float32 multiply-add with both scales
-            float sq[Gated ? NI : 1];
+        // A step is one scale block.  Each product of 128 positions starts from
+        // zero and is added to the sums with its two scales by vector
+        // instructions, three products later, so that they run beside the
+        // matrix instructions.  A turn is one m fragment.
+        constexpr int kFree = MI - 1, kPerTurn = (kLoads + kFree - 1) / kFree;
+        constexpr int kAll = MI * NI, kScales = Gated ? NI : 1;
+        i32x8 q[NI], p[2];
+        float sp[2], sq[kScales], sc[4];
+        f32x4 part[4];
 #pragma unroll
-            for (int h = 0; h < (Gated ? NI : 1); ++h) {
-                const int32_t row = tile_row<Gated>(job.q, (wn * NI + h) * 16);
-                const float* p = job.q_scales + (int64_t)(row >> 7) * kb + s;
-                sq[h] = MX_CAN_LOAD(p, 4, kSiteGemmScale) ? *p : 0.0f;
-            }
-            i32x8 q[NI];
+        for (int r = 0; r < 4; ++r) {
+            part[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            sc[r] = 0.0f;
+        }
+        auto scale = [&](int i) {                       // of row (16-row block i's) or column block
+            return *reinterpret_cast<const float*>(lds + at * S::kSlot + S::kPBytes + S::kQBytes +
+                                                   i * 4);
+        };
+        auto row_scale = [&](int i) { return scale((i * 2 + wm) * 16 + (lane & 15)); };
+        auto add = [&](int n) {                         // product n - 3
+            const int m = (n + kAll - 3) % kAll;
 #pragma unroll
-            for (int j = 0; j < NI; ++j) q[j] = fq.get_fp8(j);
+            for (int d = 0; d < 4; ++d)
+                acc[m / NI][m % NI][d] =
+                    fmaf(part[(n + 1) & 3][d], sc[(n + 1) & 3], acc[m / NI][m % NI][d]);
+        };
+        auto multiply = [&](int64_t s, auto next, bool more) {
+            constexpr bool kNext = decltype(next)::value;
+            float sq_next[kScales];
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const int32_t m = (i * 2 + wm) * 16 + (lane & 15);
-                const int32_t mc = m < job.m_rows ? m : job.m_rows - 1;
-                const float* ps = job.p_scales + (int64_t)mc * kb + s;
-                const float sp = MX_CAN_LOAD(ps, 4, kSiteGemmScale) ? *ps : 0.0f;
-                const i32x8 p = fp.get_fp8(i);
+            for (int t = 0; t < MI; ++t) {
+                if (t < kFree) {
+                    p[(t + 1) & 1] = fp.get_fp8(t + 1);
+                    sp[(t + 1) & 1] = row_scale(t + 1);
+                    if (more) {
+                        if (t == 0)
+                            loads.scales(job, lds + S::next(S::next(at)) * S::kSlot, s + 2);
+                        load_ahead(s, t * kPerTurn, (t + 1) * kPerTurn);
+                    }
+                }
+                if (kNext && t == kFree) {
+                    if (more) wait_for_all_but<kLoads>();
+                    else wait_for_loads();
+                    __syncthreads();                    // step s + 1 is there, step s is read
+                    next_slot();
+                    if (more) loads.next();
+                    p[(t + 1) & 1] = fp.get_fp8(0);
+                    sp[(t + 1) & 1] = row_scale(0);
+#pragma unroll
+                    for (int h = 0; h < kScales; ++h) sq_next[h] = scale(128 + wn * NI + h);
+                }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
-                    const f32x4 part = mfma_fp8(q[j], p, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                    const float sc = sp * sq[Gated ? j : 0];
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) acc[i][j][d] = fmaf(part[d], sc, acc[i][j][d]);
+                    const int n = t * NI + j;
+                    add(n);
+                    part[n & 3] = mfma_fp8(q[j], p[t & 1], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                    sc[n & 3] = sp[t & 1] * sq[Gated ? j : 0];
+                    if (kNext && t == kFree) q[j] = fq.get_fp8(j);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            other_tile(s);
-        }
+            if (kNext) {
+#pragma unroll
+                for (int h = 0; h < kScales; ++h) sq[h] = sq_next[h];
+            }
+        };
+        wait_for_loads();
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NI; ++j) q[j] = fq.get_fp8(j);
+        p[0] = fp.get_fp8(0);
+        sp[0] = row_scale(0);
+#pragma unroll
+        for (int h = 0; h < kScales; ++h) sq[h] = scale(128 + wn * NI + h);
+        int64_t s = 0;
+        for (; s + 1 < whole; ++s) multiply(s, std::true_type{}, s + 2 < whole);
+        multiply(s, std::false_type{}, false);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) add(n);
     } else {
         // A step is 2 MI turns of one m fragment and eight matrix instructions.
         // Fragments are read three turns ahead, those of the next step's first
         // turns in the last three; so the barrier between two steps stands
         // before these, and the matrix instructions run across it.  The loads
-        // of a tile begin when the barrier frees its memory, a few per turn,
-        // and have a whole step to arrive.
+        // of a tile begin when the barrier frees its memory, a few per turn:
+        // with two slots those of step s + 1, most of them in step s, with three
+        // those of step s + 2.
         constexpr int kTurns = 2 * MI, kFree = kTurns - 3;
-        constexpr int kPerTurn = (2 * kLoads + kTurns - 1) / kTurns;
+        constexpr int kPerTurn = Wide ? (2 * kLoads + kTurns - 1) / kTurns
+                                      : (kLoads + kFree - 1) / kFree;
         constexpr int kSecond = MI < kFree ? MI : kFree;  // turns that read the second half of q
         u32x4 q[2][NI], p[4];
         // turns after kFree that still read the first half of q
@@ -511,8 +620,9 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                 p[2] = fp.get(2 % MI, 2 / MI);
             }
         };
-        // Next: step s + 1 is whole and follows.  rest: of its loads, those after
-        // the first three turns' are still to be set off; more: step s + 2 is whole.
+        // Next: step s + 1 is whole and follows.  more: step s + 2 is whole.
+        // rest (wide): of the loads of step s + 1, those after the first three
+        // turns' are still to be set off.
         auto multiply = [&](int64_t s, auto next, bool rest, bool more) {
             constexpr bool kNext = decltype(next)::value;
 #pragma unroll
@@ -523,19 +633,23 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                     for (int j = 0; j < NI; ++j)
                         if (j * kSecond / NI == t) q[1][j] = fq.get(j, 1);
                 }
+                if (!Wide && kNext && t < kFree && more)
+                    load_ahead(s, t * kPerTurn, (t + 1) * kPerTurn);
                 if (kNext && t == kFree) {
-                    wait_for_loads();
+                    if (!Wide && more) wait_for_all_but<kLoads>();
+                    else wait_for_loads();
                     __syncthreads();                    // step s + 1 is there, step s is read
-                    other_tile(s);
-                    if (rest) loads.next();
+                    next_slot();
+                    if (Wide ? rest : more) loads.next();
                 }
                 if (kNext && t >= kFree) first_fragments(t - kFree);
-                if (kNext && (t < kFree ? rest : more)) {
+                if (Wide && kNext && (t < kFree ? rest : more)) {
                     const int turn = t < kFree ? t + 3 : t - kFree;
+                    const uint8_t* slot = lds + S::next(at) * S::kSlot;
 #pragma unroll
                     for (int i = turn * kPerTurn; i < (turn + 1) * kPerTurn; ++i)
                         if (i < kLoads)
-                            loads.template piece<true>(job, lds, t < kFree ? s + 1 : s + 2, i,
+                            loads.template piece<true>(job, slot, t < kFree ? s + 1 : s + 2, i,
                                                        kLoads - 8);
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -545,35 +659,35 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        auto tail = [&]() {                             // zeros past the end of the last step
-            const int64_t s = whole;
-            zero_tail<S::kP>(lds + (s & 1) * kTileBytes, (int)(job.len - s * S::kStep));
-            zero_tail<S::kQ>(lds + (2 + (s & 1)) * kTileBytes, (int)(job.len - s * S::kStep));
+        auto tail = [&](int slot) {                     // zeros past the end of the last step
+            const int valid = (int)(job.len - whole * S::kStep);
+            zero_tail<S::kP, S::kRows>(lds + slot * S::kSlot, valid);
+            zero_tail<S::kQ, kTileN>(lds + slot * S::kSlot + S::kPBytes, valid);
             __syncthreads();
         };
         if (a.aligned && steps > 0) {
             wait_for_loads();
             __syncthreads();
-            if (whole == 0) tail();
+            if (whole == 0) tail(0);
             first_fragments(-1);
             int64_t s = 0;
             for (; s + 1 < whole; ++s) multiply(s, std::true_type{}, s > 0, s + 2 < whole);
             const bool ragged = steps > whole && whole > 0;
-            if (ragged) loads.step(job, lds, whole);
+            if (ragged) loads.step(job, lds, whole, S::next(at));
             multiply(s, std::false_type{}, false, false);
             if (ragged) {
                 wait_for_loads();
                 __syncthreads();
-                tail();
-                other_tile(s);
+                next_slot();
+                tail(at);
                 first_fragments(-1);
                 multiply(whole, std::false_type{}, false, false);
             }
         } else {
             for (int64_t s = 0; s < steps; ++s) {
                 __syncthreads();
-                stage_elements<S::kP, false>(job.p, lds, s, job.len);
-                stage_elements<S::kQ, Gated>(job.q, lds + 2 * kTileBytes, s, job.len);
+                stage_elements<S::kP, false, S::kRows>(job.p, lds, s, job.len);
+                stage_elements<S::kQ, Gated, kTileN>(job.q, lds + S::kPBytes, s, job.len);
                 __syncthreads();
                 first_fragments(-1);
                 multiply(0, std::false_type{}, false, false);
@@ -582,21 +696,22 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
     }
     __syncthreads();                                    // the tiles are read
     advance();
-    float* stage = reinterpret_cast<float*>(lds + 4 * kTileBytes) + wave * 16 * kStageRow;
-    if (a.out_dtype == 2) store_tile<BF16, M, Gated, MI>(a, job, acc, stage, wm, wn);
-    else if (a.out_dtype == 1) store_tile<F16, M, Gated, MI>(a, job, acc, stage, wm, wn);
-    else store_tile<F32, M, Gated, MI>(a, job, acc, stage, wm, wn);
+    float* stage = reinterpret_cast<float*>(lds + S::kSlots * S::kSlot) + wave * 16 * S::kStageRow;
+    constexpr int kCols = S::kStageCols;
+    if (a.out_dtype == 2) store_tile<BF16, M, Gated, kCols, MI>(a, job, acc, stage, wm, wn);
+    else if (a.out_dtype == 1) store_tile<F16, M, Gated, kCols, MI>(a, job, acc, stage, wm, wn);
+    else store_tile<F32, M, Gated, kCols, MI>(a, job, acc, stage, wm, wn);
 }
-
-__device__ __forceinline__ int32_t m_tiles(int32_t rows) { return (rows + kTileM - 1) / kTileM; }
 
 // Forward and row-gradient products: a persistent grid walks the tiles of all
 // segments, whose number only the device knows.
-template <typename T, Mode M, bool Gated>
+template <typename T, Mode M, bool Gated, bool Wide>
 __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
-    __shared__ __align__(16) uint8_t lds[4 * kTileBytes + kStageBytes];
+    using S = Tiles<T, M, Gated, Wide>;
+    __shared__ __align__(16) uint8_t lds[S::kLds];
     __shared__ int32_t first_tile[kMaxExperts + 1];
     __shared__ int32_t wave_total[kWaves];
+    auto m_tiles = [](int32_t rows) { return (rows + S::kRows - 1) / S::kRows; };
     count_row_tiles<kThreads>(a, first_tile, wave_total, m_tiles);
     const int32_t cols_per_tile = Gated ? kTileN / 2 : kTileN;
     const int32_t n_tiles = (int32_t)((a.out_cols + cols_per_tile - 1) / cols_per_tile);
@@ -638,7 +753,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
     };
     int64_t t = begin + blockIdx.x / kXcds;
     if (t >= end) return;
-    Loaders<T, M, Gated> loads;
+    Loaders<T, M, Gated, Wide> loads;
     TileJob job = job_of(t);
     loads.start(a, job, lds);
     while (true) {
@@ -649,10 +764,13 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
             next_job = job_of(next);
             loads.start(a, next_job, lds);
         };
-        if (job.m_rows <= 64) run_tile<T, M, Gated, 2>(a, job, lds, loads, advance);
-        else if (job.m_rows <= 128) run_tile<T, M, Gated, 4>(a, job, lds, loads, advance);
-        else if (job.m_rows <= 192) run_tile<T, M, Gated, 6>(a, job, lds, loads, advance);
-        else run_tile<T, M, Gated, 8>(a, job, lds, loads, advance);
+        if (job.m_rows <= 64) run_tile<T, M, Gated, Wide, 2>(a, job, lds, loads, advance);
+        else if (!Wide || job.m_rows <= 128)
+            run_tile<T, M, Gated, Wide, 4>(a, job, lds, loads, advance);
+        else if constexpr (Wide) {
+            if (job.m_rows <= 192) run_tile<T, M, Gated, Wide, 6>(a, job, lds, loads, advance);
+            else run_tile<T, M, Gated, Wide, 8>(a, job, lds, loads, advance);
+        }
         if (next >= end) return;
         t = next;
         job = next_job;
@@ -663,7 +781,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
 // of its expert's segment.
 template <typename T>
 __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs a) {
-    __shared__ __align__(16) uint8_t lds[4 * kTileBytes + kStageBytes];
+    __shared__ __align__(16) uint8_t lds[Tiles<T, kWeightGrad, false, true>::kLds];
     const int32_t mt = (int32_t)((a.out_rows + kTileM - 1) / kTileM);
     const int32_t nt = (int32_t)((a.out_cols + kTileN - 1) / kTileN);
     const int32_t tiles = mt * nt;
@@ -691,14 +809,14 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs 
         }
         return false;
     };
-    Loaders<T, kWeightGrad, false> loads;
+    Loaders<T, kWeightGrad, false, true> loads;
     TileJob job;
     if (!find(job)) return;
     loads.start(a, job, lds);
     while (true) {
         TileJob next_job;
         bool more = false;
-        run_tile<T, kWeightGrad, false, 8>(a, job, lds, loads, [&]() {
+        run_tile<T, kWeightGrad, false, true, 8>(a, job, lds, loads, [&]() {
             t += gridDim.x / kXcds;
             more = find(next_job);
             if (more) loads.start(a, next_job, lds);
@@ -714,6 +832,13 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs 
 #endif
 static_assert(MXMOE_GEMM_GROUPS % kXcds == 0, "every XCD has the same number of workgroups");
 
+// Rows per expert (of the array, the counts are on the device) up to which the
+// narrow tiles run.
+#ifndef MXMOE_GEMM_NARROW_ROWS
+#define MXMOE_GEMM_NARROW_ROWS 160
+#endif
+constexpr int64_t kNarrowRows = MXMOE_GEMM_NARROW_ROWS;
+
 template <typename... KArgs>
 hipError_t start(void (*kernel)(KArgs...), const GemmArgs& a, hipStream_t stream) {
     launch_kernel(kernel, dim3(MXMOE_GEMM_GROUPS), dim3(kThreads), 0, stream, nullptr, nullptr, a);
@@ -724,16 +849,21 @@ hipError_t start(void (*kernel)(KArgs...), const GemmArgs& a, hipStream_t stream
 
 hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t stream) {
     if (a.dtype == 3)
-        return a.gated ? start(gemm_rows_kernel<FP8, kForward, true>, a, stream)
-                       : start(gemm_rows_kernel<FP8, kForward, false>, a, stream);
-    if (a.dtype == 1) {
-        if (a.transposed) return start(gemm_rows_kernel<F16, kRowGrad, false>, a, stream);
-        return a.gated ? start(gemm_rows_kernel<F16, kForward, true>, a, stream)
-                       : start(gemm_rows_kernel<F16, kForward, false>, a, stream);
-    }
-    if (a.transposed) return start(gemm_rows_kernel<BF16, kRowGrad, false>, a, stream);
-    return a.gated ? start(gemm_rows_kernel<BF16, kForward, true>, a, stream)
-                   : start(gemm_rows_kernel<BF16, kForward, false>, a, stream);
+        return a.gated ? start(gemm_rows_kernel<FP8, kForward, true, false>, a, stream)
+                       : start(gemm_rows_kernel<FP8, kForward, false, false>, a, stream);
+    const bool wide = a.num_rows > kNarrowRows * a.num_experts;
+    auto go = [&](auto type) {
+        using T = decltype(type);
+        if (a.transposed)
+            return wide ? start(gemm_rows_kernel<T, kRowGrad, false, true>, a, stream)
+                        : start(gemm_rows_kernel<T, kRowGrad, false, false>, a, stream);
+        if (a.gated)
+            return wide ? start(gemm_rows_kernel<T, kForward, true, true>, a, stream)
+                        : start(gemm_rows_kernel<T, kForward, true, false>, a, stream);
+        return wide ? start(gemm_rows_kernel<T, kForward, false, true>, a, stream)
+                    : start(gemm_rows_kernel<T, kForward, false, false>, a, stream);
+    };
+    return a.dtype == 1 ? go(F16{}) : go(BF16{});
 }
 
 hipError_t launch_grouped_wgrad(const GemmArgs& a, hipStream_t stream) {
