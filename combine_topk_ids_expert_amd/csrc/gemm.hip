@@ -835,7 +835,7 @@ static_assert(MXMOE_GEMM_GROUPS % kXcds == 0, "every XCD has the same number of 
 // Rows per expert (of the array, the counts are on the device) up to which the
 // narrow tiles run.
 #ifndef MXMOE_GEMM_NARROW_ROWS
-#define MXMOE_GEMM_NARROW_ROWS 160
+#define MXMOE_GEMM_NARROW_ROWS 96
 #endif
 constexpr int64_t kNarrowRows = MXMOE_GEMM_NARROW_ROWS;
 

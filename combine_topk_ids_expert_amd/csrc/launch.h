@@ -108,8 +108,7 @@ struct GemmArgs {
     bool transposed;          // w is [E][len][out_cols]
     bool accumulate;          // weight gradient: add to out
     bool aligned;             // rows of x and w are 16-byte aligned
-    bool whole_units;         // 4 bits: len is a multiple of 128, scales and zeros aligned to
-                              // what 128 positions have of them
+    bool whole_units;         // 4 bits: len is a multiple of 128 and at least 8 groups
     bool vector_store;        // rows of out (and gate_up) take 16-byte stores
 };
 

@@ -7,7 +7,7 @@
 // with w either of x's 16-bit type or 4 bits with one scale (and zero point)
 // per `group` positions:  w = (q - z) s.  For those,
 //
-//   sum_{k in G} (q - z) x = sum_k (B + q) x - (B + z) sum_k x,
+//   sum_{k in G} (q - z) x = -(B + z) sum_k x + sum_k (B + q) x,
 //
 // where B + q is the 16-bit number whose low mantissa bits are q (B = 128 in
 // bf16, 1024 in fp16): one AND-OR makes two of them, every B + q is exact,
@@ -74,6 +74,10 @@ struct Tile {
     int64_t row0;
 };
 
+// kPlain: len is a multiple of 128 and holds 8 groups or more, no zero points;
+// kZeros: the same with them; kAny: any.
+enum Form { kPlain, kZeros, kAny };
+
 // One unit's weights of a lane: of each 16-row block, 32 positions of row
 // l & 15 and the scales and zero points of the unit's 128 / Group groups.
 template <int Group>
@@ -84,20 +88,30 @@ struct Unit {
     uint32_t z[4];
 };
 
+// The scales and zero points of 8 groups in a row, of row `lane` of the tile: a
+// load for all 64 rows.  (Loads by the unit, 2 to 8 bytes from each of 16 rows
+// four times over, cost the L1 cache twice what the weights do.)
+struct Scales {
+    uint32_t s[4], z[2];
+};
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, -1, 0x00020000);
 }
 
 // Where a lane's weights lie: uniform bases of the tile's gate (or only) and up
-// rows, and the lane's row below them for each block.
-template <typename T, bool Gated, int Group>
+// rows, and the byte and scale offsets of the lane's row of each block.
+template <bool Gated, int Group, Form F>
 struct Weights {
+    static constexpr int kScales = Unit<Group>::kScales;
     const uint8_t* base[2];
     const uint16_t* scales[2];
     const uint8_t* zeros[2];
-    uint32_t row[4];
+    uint32_t w_at[4], s_at[4];
+    uint32_t row;                 // the tile's row `lane`, for the scales
 
     __device__ __forceinline__ void init(const GemmArgs& a, const Tile& t) {
+        const int lane = threadIdx.x & 63;
         const int64_t groups = a.len / Group;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -111,131 +125,234 @@ struct Weights {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // gated tiles alternate gate and up blocks
-            const int r = (Gated ? (j >> 1) * 16 : j * 16) + (int)(threadIdx.x & 15);
-            row[j] = (uint32_t)(r < last ? r : last);
+            const int r = (Gated ? (j >> 1) * 16 : j * 16) + (lane & 15);
+            const uint32_t at = (uint32_t)(r < last ? r : last);
+            w_at[j] = at * (uint32_t)a.w_row_bytes + (lane >> 4) * 16;
+            s_at[j] = at * (uint32_t)groups;
         }
+        const int r = (Gated ? (lane >> 5) * 16 : (lane >> 4) * 16) + (lane & 15);
+        row = (uint32_t)(r < last ? r : last);
     }
-    // The unit from position k0 on; positions past the end read the last ones
-    // there are (x is zero there).
-    __device__ __forceinline__ void load(const GemmArgs& a, int64_t k0, Unit<Group>& u) const {
-        constexpr int kScales = Unit<Group>::kScales;
-        int32_t k = (int32_t)k0 + ((threadIdx.x & 63) >> 4) * 32;
-        k = k < a.len ? k : (int32_t)a.len - 32;
+    // The unit's words; its scales come from `scales`.
+    __device__ __forceinline__ void load_words(uint32_t k0, Unit<Group>& u) const {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint8_t* b = base[Gated ? j & 1 : 0];
-            const uint32_t at = row[j] * (uint32_t)a.w_row_bytes + (uint32_t)(k / 2);
             u.w[j] = u32x4{0u, 0u, 0u, 0u};
-            if (MX_CAN_LOAD(b + at, 16, kSiteGemmLoad))
-                u.w[j] = __builtin_amdgcn_raw_buffer_load_b128(buffer(b), at, 0, 0);
+            if (MX_CAN_LOAD(b + w_at[j] + k0 / 2, 16, kSiteGemmLoad))
+                u.w[j] = __builtin_amdgcn_raw_buffer_load_b128(buffer(b), w_at[j], k0 / 2, 0);
         }
-        const uint32_t groups = (uint32_t)(a.len / Group), g0 = (uint32_t)(k0 / Group);
+    }
+    // Groups g0 .. + 8 of the tile's row `lane`; of the last ones, what there is.
+    __device__ __forceinline__ void load_scales(const GemmArgs& a, uint32_t g0, Scales& v) const {
+        const uint32_t groups = (uint32_t)a.len / Group;
+        const uint32_t from = g0 + 8 <= groups ? g0 : groups - 8, skip = g0 - from;
+        const int lane = threadIdx.x & 63, half = Gated ? (lane >> 4) & 1 : 0;
+        const uint32_t at = row * groups + from;
+        const uint16_t* sp = scales[half] + at;
+        uint64_t lo = 0, hi = 0;
+        struct __attribute__((packed, aligned(2))) Eight { uint64_t v[2]; };
+        struct __attribute__((packed, aligned(1))) Bytes { uint64_t v; };
+        if (MX_CAN_LOAD(sp, 16, kSiteGemmScale)) {
+            const Eight e = *reinterpret_cast<const Eight*>(sp);
+            lo = e.v[0];
+            hi = e.v[1];
+        }
+        uint64_t zv = 0;
+        if (F == kZeros && MX_CAN_LOAD(zeros[half] + at, 8, kSiteGemmScale))
+            zv = reinterpret_cast<const Bytes*>(zeros[half] + at)->v;
+        if (skip != 0) {
+            const uint32_t bits = skip * 16;
+            lo = bits < 64 ? lo >> bits | hi << (64 - bits) : hi >> (bits - 64);
+            hi = bits < 64 ? hi >> bits : 0;
+            zv >>= skip * 8;
+        }
+        v.s[0] = (uint32_t)lo;
+        v.s[1] = (uint32_t)(lo >> 32);
+        v.s[2] = (uint32_t)hi;
+        v.s[3] = (uint32_t)(hi >> 32);
+        v.z[0] = (uint32_t)zv;
+        v.z[1] = (uint32_t)(zv >> 32);
+    }
+    // Unit i of the 8 groups' to the lanes that hold its weights.
+    __device__ __forceinline__ static void take(const Scales& v, int i, Unit<Group>& u) {
+        const int r16 = threadIdx.x & 15;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint16_t* b = scales[Gated ? j & 1 : 0];
-            const uint8_t* zb = zeros[Gated ? j & 1 : 0];
-            const uint32_t at = row[j] * groups + g0;
-            if (a.whole_units) {
-                uint32_t s[2] = {0u, 0u}, z = 0u;
-                if (MX_CAN_LOAD(b + at, 2 * kScales, kSiteGemmScale)) {
-                    if constexpr (kScales == 4) {
-                        const u32x2 v =
-                            __builtin_amdgcn_raw_buffer_load_b64(buffer(b), at * 2, 0, 0);
-                        s[0] = v[0];
-                        s[1] = v[1];
-                    } else if constexpr (kScales == 2) {
-                        s[0] = __builtin_amdgcn_raw_buffer_load_b32(buffer(b), at * 2, 0, 0);
-                    } else {
-                        s[0] = __builtin_amdgcn_raw_buffer_load_b16(buffer(b), at * 2, 0, 0);
-                    }
-                }
-                if (a.w_zeros != nullptr && MX_CAN_LOAD(zb + at, kScales, kSiteGemmScale)) {
-                    if constexpr (kScales == 4)
-                        z = __builtin_amdgcn_raw_buffer_load_b32(buffer(zb), at, 0, 0);
-                    else if constexpr (kScales == 2)
-                        z = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(buffer(zb), at, 0, 0);
-                    else
-                        z = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(buffer(zb), at, 0, 0);
-                }
-                u.s[j][0] = s[0];
-                if constexpr (kScales == 4) u.s[j][1] = s[1];
-                u.z[j] = z;
+            const int from = (j * 16 + r16) * 4;
+            auto get = [&](uint32_t x) {
+                return (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)x);
+            };
+            if constexpr (kScales == 4) {
+                u.s[j][0] = get(v.s[2 * i]);
+                u.s[j][1] = get(v.s[2 * i + 1]);
+                if (F == kZeros) u.z[j] = get(v.z[i]);
+            } else if constexpr (kScales == 2) {
+                u.s[j][0] = get(v.s[i]);
+                if (F == kZeros) u.z[j] = get(v.z[i / 2] >> (16 * (i % 2)));
             } else {
-                u.z[j] = 0;
+                u.s[j][0] = get(v.s[i / 2] >> (16 * (i % 2))) & 0xffffu;
+                if (F == kZeros) u.z[j] = get(v.z[i / 4] >> (8 * (i % 4)));
+            }
+        }
+    }
+    // A unit that may be cut short, or whose scales are not aligned: positions
+    // and groups past the end read the last ones there are.
+    __device__ __forceinline__ void load_any(const GemmArgs& a, uint32_t k0, Unit<Group>& u) const {
+        const uint32_t len = (uint32_t)a.len, own = ((threadIdx.x & 63) >> 4) * 32;
+        const uint32_t k = k0 + own < len ? k0 : len - 32 - own;    // may wrap, own is added back
+        const uint32_t groups = len / Group, g0 = k0 / Group;
 #pragma unroll
-                for (int g = 0; g < kScales; ++g) {
-                    const uint32_t i = at + (g0 + g < groups ? g : groups - 1 - g0);
-                    const uint32_t v = MX_CAN_LOAD(b + i, 2, kSiteGemmScale) ? b[i] : 0;
-                    u.s[j][g / 2] = g % 2 ? u.s[j][g / 2] | v << 16 : v;
-                    if (a.w_zeros != nullptr && MX_CAN_LOAD(zb + i, 1, kSiteGemmScale))
-                        u.z[j] |= (uint32_t)zb[i] << (8 * g);
-                }
+        for (int j = 0; j < 4; ++j) {
+            const uint8_t* b = base[Gated ? j & 1 : 0];
+            const uint32_t at = w_at[j] - own / 2 + (k + own) / 2;
+            u.w[j] = u32x4{0u, 0u, 0u, 0u};
+            if (MX_CAN_LOAD(b + at, 16, kSiteGemmLoad))
+                u.w[j] = *reinterpret_cast<const u32x4*>(b + at);
+            u.z[j] = 0;
+#pragma unroll
+            for (int g = 0; g < kScales; ++g) {
+                const uint32_t i = s_at[j] + (g0 + g < groups ? g0 + g : groups - 1);
+                const uint16_t* sb = scales[Gated ? j & 1 : 0];
+                const uint32_t v = MX_CAN_LOAD(sb + i, 2, kSiteGemmScale) ? sb[i] : 0;
+                u.s[j][g / 2] = g % 2 ? u.s[j][g / 2] | v << 16 : v;
+                const uint8_t* zb = zeros[Gated ? j & 1 : 0];
+                if (a.w_zeros != nullptr && MX_CAN_LOAD(zb + i, 1, kSiteGemmScale))
+                    u.z[j] |= (uint32_t)zb[i] << (8 * g);
             }
         }
     }
 };
 
-// The wave's share of a tile's sums: units wave, wave + 4, ... of the
-// contraction, the first of them in `u`, each unit's weights loaded while the
-// one before is multiplied.
-template <typename T, bool Gated, int Group>
-__device__ __forceinline__ void multiply(const GemmArgs& a, const Tile& t,
-                                         const Weights<T, Gated, Group>& weights, Unit<Group> u,
-                                         f32x4 (&acc)[4]) {
-    constexpr int kScales = Unit<Group>::kScales, kSteps = Group / 32;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int g = lane >> 4, r16 = lane & 15;
-    const uint8_t* xb = a.x + t.row0 * a.x_row_bytes;
-    const uint32_t x_at =
-        (uint32_t)(r16 < t.rows ? r16 : t.rows - 1) * (uint32_t)a.x_row_bytes + g * 16;
-    for (int64_t k0 = (int64_t)wave * kUnit; k0 < a.len; k0 += kWaves * kUnit) {
-        u32x4 x[4];
+// A lane's share of x in a unit: positions 8 (l >> 4) .. + 8 of each 32 of row
+// l & 15; zeros past the end.
+struct Rows {
+    const uint8_t* base;
+    uint32_t at;
+
+    __device__ __forceinline__ void init(const GemmArgs& a, const Tile& t) {
+        const int lane = threadIdx.x & 63, r = lane & 15;
+        base = a.x + t.row0 * a.x_row_bytes;
+        at = (uint32_t)(r < t.rows ? r : t.rows - 1) * (uint32_t)a.x_row_bytes + (lane >> 4) * 16;
+    }
+    template <Form F>
+    __device__ __forceinline__ void load(const GemmArgs& a, uint32_t k0, u32x4 (&x)[4]) const {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+            const uint32_t k = k0 + q * 32;
             x[q] = u32x4{0u, 0u, 0u, 0u};
-            const uint32_t k = (uint32_t)k0 + q * 32;
-            if (k < a.len && MX_CAN_LOAD(xb + x_at + k * 2, 16, kSiteGemmLoad))
-                x[q] = __builtin_amdgcn_raw_buffer_load_b128(buffer(xb), x_at, k * 2, 0);
+            if ((F != kAny || k < a.len) && MX_CAN_LOAD(base + at + k * 2, 16, kSiteGemmLoad))
+                x[q] = __builtin_amdgcn_raw_buffer_load_b128(buffer(base), at, k * 2, 0);
         }
-        Unit<Group> next = u;
-        if (k0 + kWaves * kUnit < a.len) weights.load(a, k0 + kWaves * kUnit, next);
-        uint32_t w[4][4];
+    }
+};
+
+// Adds one unit's products to the sums: per group the sum of (B + q) x, which
+// starts from -(B + z) sum x, times the scale.
+template <typename T, int Group, Form F>
+__device__ __forceinline__ void add_unit(const GemmArgs& a, const Unit<Group>& u,
+                                         const u32x4 (&x)[4], f32x4 (&acc)[4]) {
+    constexpr int kScales = Unit<Group>::kScales, kSteps = Group / 32;
+    const u32x4 ones = {Bias<T>::one, Bias<T>::one, Bias<T>::one, Bias<T>::one};
+    u32x4 xo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+    for (int q = 0; q < 4; ++q) xo[q] = nibble_order(x[q]);
+    f32x4 start[kScales];                               // -(B + 8) sum x, or sum x
 #pragma unroll
-            for (int q = 0; q < 4; ++q) w[j][q] = u.w[j][q];
-            transpose_groups(w[j]);
-        }
-        const u32x4 ones = {Bias<T>::one, Bias<T>::one, Bias<T>::one, Bias<T>::one};
+    for (int gr = 0; gr < kScales; ++gr) {
+        start[gr] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)
+            start[gr] = mfma_16(T{}, xo[gr * kSteps + st], ones, start[gr]);
+    }
+    const bool zeros = F == kZeros || (F == kAny && a.w_zeros != nullptr);
+    if (!zeros) {
+#pragma unroll
+        for (int gr = 0; gr < kScales; ++gr)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) start[gr][d] *= -(Bias<T>::value + 8.0f);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = u.w[j][q];
+        transpose_groups(w);
 #pragma unroll
         for (int gr = 0; gr < kScales; ++gr) {
-            if (k0 + gr * Group >= a.len) break;
-            f32x4 part[4], sx = {0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 part = start[gr];
+            if (zeros) {
+                const float z = -(Bias<T>::value + (float)((u.z[j] >> (8 * gr)) & 0xffu));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int d = 0; d < 4; ++d) part[d] *= z;
+            }
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
                 const int q = gr * kSteps + st;
-                const u32x4 xo = nibble_order(x[q]);
-                sx = mfma_16(T{}, xo, ones, sx);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    part[j] = mfma_16(T{}, xo, widen4<T>(w[j][q]), part[j]);
+                part = mfma_16(T{}, xo[q], widen4<T>(w[q]), part);
             }
+            const float s = to_f32(T{}, (uint16_t)(u.s[j][gr / 2] >> (16 * (gr % 2))));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float s = to_f32(T{}, (uint16_t)(u.s[j][gr / 2] >> (16 * (gr % 2))));
-                const float z = Bias<T>::value + (a.w_zeros != nullptr
-                                                      ? (float)((u.z[j] >> (8 * gr)) & 0xffu)
-                                                      : 8.0f);
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    acc[j][d] = fmaf(s, fmaf(-z, sx[d], part[j][d]), acc[j][d]);
-            }
+            for (int d = 0; d < 4; ++d) acc[j][d] = fmaf(s, part[d], acc[j][d]);
         }
-        u = next;
+        __builtin_amdgcn_sched_barrier(0);              // one block's words at a time
     }
 }
+
+// What one unit takes from memory.
+template <int Group>
+struct Stage {
+    Unit<Group> u;
+    u32x4 x[4];
+};
+
+// The wave's share of a tile: a quarter of the contraction's units, in a row.
+template <typename T, bool Gated, int Group, Form F>
+struct Tiling {
+    static constexpr int kBatch = 8 / Unit<Group>::kScales;     // units of 8 groups
+    Weights<Gated, Group, F> weights;
+    Rows rows;
+    uint32_t k0, end;             // positions
+
+    __device__ __forceinline__ void init(const GemmArgs& a, const Tile& t) {
+        weights.init(a, t);
+        rows.init(a, t);
+        const uint32_t units = ((uint32_t)a.len + kUnit - 1) / kUnit;
+        const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        k0 = units * wave / kWaves * kUnit;
+        end = units * (wave + 1) / kWaves * kUnit;
+    }
+    // Sets off the loads of the first unit.
+    __device__ __forceinline__ void start(const GemmArgs& a, Stage<Group>& s, Scales& v) const {
+        if (k0 >= end) return;
+        load(a, k0, s);
+        if (F != kAny) weights.load_scales(a, k0 / Group, v);
+    }
+    __device__ __forceinline__ void load(const GemmArgs& a, uint32_t k, Stage<Group>& s) const {
+        if (k >= end) return;
+        if constexpr (F == kAny) weights.load_any(a, k, s.u);
+        else weights.load_words(k, s.u);
+        rows.template load<F>(a, k, s.x);
+    }
+    // The sums over the wave's units, each loaded while the one before is
+    // multiplied; the scales are loaded 8 groups ahead.
+    __device__ __forceinline__ void multiply(const GemmArgs& a, Stage<Group> (&s)[2], Scales v,
+                                             f32x4 (&acc)[4]) const {
+        for (uint32_t k = k0; k < end;) {
+            Scales next = v;
+            if (F != kAny && k + kBatch * kUnit < end)
+                weights.load_scales(a, (k + kBatch * kUnit) / Group, next);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i, k += kUnit) {
+                if (k >= end) break;
+                load(a, k + kUnit, s[(i + 1) & 1]);
+                if (F != kAny) weights.take(v, i, s[i & 1].u);
+                add_unit<T, Group, F>(a, s[i & 1].u, s[i & 1].x, acc);
+            }
+            v = next;
+        }
+    }
+};
 
 // The waves' sums added in order through LDS, [wave][row][column], and written.
 template <bool Gated>
@@ -274,7 +391,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Tile& t,
 __device__ __forceinline__ int32_t row_tiles(int32_t rows) { return (rows + kRows - 1) / kRows; }
 
 // 3 waves per SIMD (at most 168 registers), each with 4 KiB of weights under way.
-template <typename T, bool Gated, int Group>
+template <typename T, bool Gated, int Group, Form F>
 __global__ __launch_bounds__(kThreads, 3) void w4_kernel(GemmArgs a) {
     __shared__ float lds[kWaves * 16 * (kCols + 1)];
     __shared__ int32_t first_tile[kMaxExperts + 1];
@@ -303,24 +420,24 @@ __global__ __launch_bounds__(kThreads, 3) void w4_kernel(GemmArgs a) {
     };
     int64_t t = begin + blockIdx.x / kXcds;
     if (t >= end) return;
-    const int64_t k0 = (int64_t)(threadIdx.x >> 6) * kUnit;
-    Weights<T, Gated, Group> weights;
-    Unit<Group> u;
+    Tiling<T, Gated, Group, F> tiling;
+    Stage<Group> stages[2];
+    Scales scales;
     Tile tile = tile_of(t);
-    weights.init(a, tile);
-    if (k0 < a.len) weights.load(a, k0, u);
+    tiling.init(a, tile);
+    tiling.start(a, stages[0], scales);
     while (true) {
         f32x4 acc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        multiply<T, Gated, Group>(a, tile, weights, u, acc);
+        tiling.multiply(a, stages, scales, acc);
         // the next tile's first unit is loaded under this one's sums
         const Tile done = tile;
         t += gridDim.x / kXcds;
         if (t < end) {
             tile = tile_of(t);
-            weights.init(a, tile);
-            if (k0 < a.len) weights.load(a, k0, u);
+            tiling.init(a, tile);
+            tiling.start(a, stages[0], scales);
         }
         finish<Gated>(a, done, acc, lds);
         if (t >= end) return;
@@ -340,11 +457,18 @@ hipError_t start(void (*kernel)(KArgs...), const GemmArgs& a, hipStream_t stream
     return hipGetLastError();
 }
 
+template <typename T, bool Gated, int Group>
+hipError_t start(const GemmArgs& a, hipStream_t stream) {
+    if (!a.whole_units) return start(w4_kernel<T, Gated, Group, kAny>, a, stream);
+    if (a.w_zeros != nullptr) return start(w4_kernel<T, Gated, Group, kZeros>, a, stream);
+    return start(w4_kernel<T, Gated, Group, kPlain>, a, stream);
+}
+
 template <typename T, bool Gated>
 hipError_t start(const GemmArgs& a, hipStream_t stream) {
-    if (a.group == 32) return start(w4_kernel<T, Gated, 32>, a, stream);
-    if (a.group == 64) return start(w4_kernel<T, Gated, 64>, a, stream);
-    return start(w4_kernel<T, Gated, 128>, a, stream);
+    if (a.group == 32) return start<T, Gated, 32>(a, stream);
+    if (a.group == 64) return start<T, Gated, 64>(a, stream);
+    return start<T, Gated, 128>(a, stream);
 }
 
 }  // namespace
