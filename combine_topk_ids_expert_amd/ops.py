@@ -23,10 +23,13 @@ import torch
 from torch import Tensor
 
 from . import (apply_shuffle_mul_sum as _combine, dispatch_rows as _dispatch,
-               dispatch_rows_fp8 as _dispatch_fp8, moe_output_memset as _memset,
+               dispatch_rows_fp8 as _dispatch_fp8, grouped_gemm as _gemm,
+               grouped_gemm_fp8 as _gemm_fp8, grouped_gemm_w4 as _gemm_w4,
+               grouped_gemm_wgrad as _wgrad, moe_output_memset as _memset,
                moe_sort as _moe_sort, prepare_dispatch as _prepare_dispatch,
                prepare_moe_input as _prepare, shuffle_rows as _shuffle,
-               zero_padding_rows as _zero_padding)
+               silu_mul_backward as _silu_backward, topk_gating as _gating,
+               topk_gating_backward as _gating_backward, zero_padding_rows as _zero_padding)
 
 __all__ = ["OPS"]
 
@@ -118,8 +121,67 @@ def moe_sort(topk_ids: Tensor, num_experts: int, local_expert_offset: int,
               workspace=workspace)
 
 
+@torch.library.custom_op("mxmoe::topk_gating", mutates_args=("topk_ids", "topk_weights"),
+                         device_types="cuda")
+def topk_gating(logits: Tensor, topk_ids: Tensor, topk_weights: Tensor, scoring: str,
+                bias: Optional[Tensor], renormalize: bool, scale: float) -> None:
+    _gating(logits, topk_ids, topk_weights, scoring=scoring, bias=bias, renormalize=renormalize,
+            scale=scale)
+
+
+@torch.library.custom_op("mxmoe::topk_gating_backward", mutates_args=("grad_logits",),
+                         device_types="cuda")
+def topk_gating_backward(logits: Tensor, topk_ids: Tensor, grad_weights: Tensor,
+                         grad_logits: Tensor, scoring: str, renormalize: bool,
+                         scale: float) -> None:
+    _gating_backward(logits, topk_ids, grad_weights, grad_logits, scoring=scoring,
+                     renormalize=renormalize, scale=scale)
+
+
+@torch.library.custom_op("mxmoe::grouped_gemm", mutates_args=("output", "gate_up"),
+                         device_types="cuda")
+def grouped_gemm(input: Tensor, weight: Tensor, expert_offsets: Tensor, output: Tensor,
+                 problem_sizes: Optional[Tensor], transpose_weight: bool, silu_mul: bool,
+                 gate_up: Optional[Tensor]) -> None:
+    _gemm(input, weight, expert_offsets, output, problem_sizes, transpose_weight=transpose_weight,
+          silu_mul=silu_mul, gate_up=gate_up)
+
+
+@torch.library.custom_op("mxmoe::grouped_gemm_fp8", mutates_args=("output",), device_types="cuda")
+def grouped_gemm_fp8(input: Tensor, input_scales: Tensor, weight: Tensor, weight_scales: Tensor,
+                     expert_offsets: Tensor, output: Tensor, problem_sizes: Optional[Tensor],
+                     silu_mul: bool) -> None:
+    _gemm_fp8(input, input_scales, weight, weight_scales, expert_offsets, output, problem_sizes,
+              silu_mul=silu_mul)
+
+
+@torch.library.custom_op("mxmoe::grouped_gemm_w4", mutates_args=("output",), device_types="cuda")
+def grouped_gemm_w4(input: Tensor, weight: Tensor, scales: Tensor, expert_offsets: Tensor,
+                    output: Tensor, problem_sizes: Optional[Tensor], zeros: Optional[Tensor],
+                    silu_mul: bool) -> None:
+    _gemm_w4(input, weight, scales, expert_offsets, output, problem_sizes, zeros=zeros,
+             silu_mul=silu_mul)
+
+
+@torch.library.custom_op("mxmoe::grouped_gemm_wgrad", mutates_args=("grad_weight",),
+                         device_types="cuda")
+def grouped_gemm_wgrad(grad_output: Tensor, input: Tensor, expert_offsets: Tensor,
+                       grad_weight: Tensor, problem_sizes: Optional[Tensor],
+                       accumulate: bool) -> None:
+    _wgrad(grad_output, input, expert_offsets, grad_weight, problem_sizes, accumulate=accumulate)
+
+
+@torch.library.custom_op("mxmoe::silu_mul_backward", mutates_args=("grad_gate_up",),
+                         device_types="cuda")
+def silu_mul_backward(grad_output: Tensor, gate_up: Tensor, expert_offsets: Tensor,
+                      grad_gate_up: Tensor, problem_sizes: Optional[Tensor]) -> None:
+    _silu_backward(grad_output, gate_up, expert_offsets, grad_gate_up, problem_sizes)
+
+
 OPS = (prepare_moe_input, prepare_dispatch, shuffle_rows, dispatch_rows, apply_shuffle_mul_sum,
-       moe_output_memset, zero_padding_rows, dispatch_rows_fp8, moe_sort)
+       moe_output_memset, zero_padding_rows, dispatch_rows_fp8, moe_sort, topk_gating,
+       topk_gating_backward, grouped_gemm, grouped_gemm_fp8, grouped_gemm_w4, grouped_gemm_wgrad,
+       silu_mul_backward)
 
 
 def _returns_nothing(*args, **kwargs) -> None:

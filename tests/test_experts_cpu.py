@@ -123,3 +123,27 @@ GATING_BACK = dict(x=P, dtype=BF16, T=10, E=64, k=8, scoring=1, renorm=0, scale=
     (dict(out=P + 1), MISALIGNED), (dict(x=P + 1), MISALIGNED), (dict(T=0), OK)])
 def test_topk_gating_backward(lib, kw, status):
     assert _call(lib.mx_topk_gating_backward, GATING_BACK, **kw) == status
+
+
+MUTATED = {
+    "topk_gating": {"topk_ids", "topk_weights"}, "topk_gating_backward": {"grad_logits"},
+    "grouped_gemm": {"output", "gate_up"}, "grouped_gemm_fp8": {"output"},
+    "grouped_gemm_w4": {"output"}, "grouped_gemm_wgrad": {"grad_weight"},
+    "silu_mul_backward": {"grad_gate_up"},
+}
+
+
+@pytest.mark.parametrize("name", sorted(MUTATED))
+def test_operator_schema_marks_the_outputs(name):
+    import torch
+    import combine_topk_ids_expert_amd.ops  # noqa: F401  (registers torch.ops.mxmoe)
+    schema = getattr(torch.ops.mxmoe, name).default._schema
+    written = {a.name for a in schema.arguments
+               if a.alias_info is not None and a.alias_info.is_write}
+    assert written == MUTATED[name] and len(schema.returns) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(flags=SILU, n=2**15, k=2**15), OK), (dict(flags=SILU, n=2**15 + 1, k=2**15), INVALID)])
+def test_gated_products_stay_in_32_bit_offsets(lib, kw, status):
+    assert _call(lib.mx_grouped_gemm, GEMM, rows=0, **kw) == status
