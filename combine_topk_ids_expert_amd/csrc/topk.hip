@@ -355,8 +355,9 @@ __global__ __launch_bounds__(kThreads, NC <= 5 ? 4 : NC <= 8 ? 3 : 2) void topk_
     }
 }
 
+// One token with a whole wave, for any k.
 template <typename T, int PER>
-__global__ __launch_bounds__(kThreads) void topk_gating_backward_kernel(GatingArgs a) {
+__global__ __launch_bounds__(kThreads) void topk_gating_backward_wave_kernel(GatingArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * kTokens + (threadIdx.x >> 6);
     if (t >= a.num_tokens) return;
@@ -434,6 +435,122 @@ __global__ __launch_bounds__(kThreads) void topk_gating_backward_kernel(GatingAr
     }
 }
 
+// The gradient with four tokens to a wave, for up to 16 picks: lane l of a
+// token's 16 holds pick l and writes experts (16 c + l) 4 + i.
+template <int J, int N, typename F>
+__device__ __forceinline__ void for_each_pick(F&& f) {
+    if constexpr (J < N) {
+        f(std::integral_constant<int, J>{});
+        for_each_pick<J + 1, N>(f);
+    }
+}
+
+template <typename T, int NC>
+__global__ __launch_bounds__(kThreads) void topk_gating_backward_kernel(GatingArgs a, bool vec) {
+    const int l = threadIdx.x & 15;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
+    const bool here = t < a.num_tokens;
+    const int E = a.num_experts;
+    using S = typename T::storage;
+    struct alignas(4 * sizeof(S)) Four { S v[4]; };
+    int id = -1;
+    float g = 0.0f, px = -kInf;
+    if (here && l < a.topk) {
+        const int32_t* ip = a.ids + t * a.topk + l;
+        const float* gp = a.weights + t * a.topk + l;
+        if (MX_CAN_LOAD(ip, 4, kSiteTopkLoad)) id = *ip;
+        if (MX_CAN_LOAD(gp, 4, kSiteTopkLoad)) g = *gp;
+        if (id >= 0 && id < E) px = logit<T>(a.logits, t * E + id);
+    }
+    const bool live = px > -kInf;                           // not NaN either
+    if (!live) {
+        id = -1;
+        g = 0.0f;
+        px = -kInf;
+    }
+    const bool rest = !a.sigmoid && !a.renormalize;         // every expert has a gradient
+    float x[NC][4], most = px, sum, d;
+    if (rest) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = (c * 16 + l) * 4 + i;
+                x[c][i] = here && e < E ? logit<T>(a.logits, t * E + e) : -kInf;
+                x[c][i] = fmaxf(x[c][i], -kInf);            // NaN becomes -inf
+                most = fmaxf(most, x[c][i]);
+            }
+    }
+    most = row_max(most);
+    if (a.sigmoid) {
+        const float s = live ? sigmoid(px) : 0.0f;
+        float ds = g;
+        if (a.renormalize) {
+            const float total = row_sum(s);
+            const float dot = row_sum(total > 0.0f ? s / total * g : 0.0f);
+            ds = total > 0.0f ? (g - dot) / total : 0.0f;
+        }
+        d = live ? a.scale * ds * s * (1.0f - s) : 0.0f;
+        sum = 0.0f;
+    } else {
+        sum = live ? exp_below(px, most) : 0.0f;
+        if (rest) {
+            sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += x[c][i] > -kInf ? exp_below(x[c][i], most) : 0.0f;
+        }
+        sum = row_sum(sum);
+        const float p = live ? exp_below(px, most) / sum : 0.0f;
+        const float dot = row_sum(p * g);
+        d = live ? a.scale * p * (rest ? g : g - dot) : 0.0f;
+        if (rest) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[c][i] = x[c][i] > -kInf
+                                  ? -a.scale * (exp_below(x[c][i], most) / sum) * dot : 0.0f;
+        }
+    }
+    if (!rest) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[c][i] = 0.0f;
+    }
+    // one pick after the other, in order: row_newbcast gives the row its lane
+    for_each_pick<0, 16>([&](auto j) {
+        if (decltype(j)::value >= a.topk) return;
+        const int at = dpp<0x150 + decltype(j)::value>(id);
+        const float v = dpp_f<0x150 + decltype(j)::value>(d);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (at == (c * 16 + l) * 4 + i) x[c][i] += v;
+    });
+    if (!here) return;
+    S* row = static_cast<S*>(a.grad_logits) + t * E;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int e = (c * 16 + l) * 4;
+        if (vec) {
+            Four f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f.v[i] = from_f32(T{}, x[c][i]);
+            if (e < E && MX_CAN_STORE(row + e, sizeof(Four), kSiteTopkOut))
+                *reinterpret_cast<Four*>(row + e) = f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e + i < E && MX_CAN_STORE(row + e + i, sizeof(S), kSiteTopkOut))
+                    row[e + i] = from_f32(T{}, x[c][i]);
+        }
+    }
+}
+
 // go(arguments, workgroups) for batches of tokens, `per_group` to a workgroup.
 template <typename T, typename F>
 hipError_t for_token_batches(const GatingArgs& a, int per_group, F&& go) {
@@ -484,10 +601,18 @@ hipError_t start(const GatingArgs& a, hipStream_t stream) {
 template <typename T>
 hipError_t start_backward(const GatingArgs& a, hipStream_t stream) {
     const int per = (a.num_experts + kWave - 1) / kWave;
+    const bool rows = a.topk <= 16;
+    const bool vec = a.num_experts % 4 == 0 &&
+                     (uintptr_t)a.grad_logits % (4 * sizeof(typename T::storage)) == 0;
     auto go = [&](auto n) {
-        return for_token_batches<T>(a, kTokens, [&](const GatingArgs& b, dim3 grid) {
-            launch_kernel(topk_gating_backward_kernel<T, decltype(n)::value>, grid, dim3(kThreads),
-                          0, stream, nullptr, nullptr, b);
+        return for_token_batches<T>(a, rows ? kThreads / 16 : kTokens, [&](const GatingArgs& b,
+                                                                         dim3 grid) {
+            if (rows)
+                launch_kernel(topk_gating_backward_kernel<T, decltype(n)::value>, grid,
+                              dim3(kThreads), 0, stream, nullptr, nullptr, b, vec);
+            else
+                launch_kernel(topk_gating_backward_wave_kernel<T, decltype(n)::value>, grid,
+                              dim3(kThreads), 0, stream, nullptr, nullptr, b);
         });
     };
     MX_PER_LANE(go)
