@@ -24,8 +24,7 @@ namespace {
 // read 192 KiB together in place of 128, as long as their matrix instructions
 // take.
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
-constexpr int kTileM = 256, kTileN = 256; // of the wide tiles
-constexpr int NI = 8;                     // 16-column blocks of a wave
+constexpr int kTileM = 256;               // of the wide tiles
 constexpr int kStepBytes = 128;           // contraction bytes of one step, a tile row in LDS
 constexpr int kXcds = 8;
 
@@ -96,15 +95,18 @@ __device__ __forceinline__ int swizzle_across(int kk) {
     return ((kk & 3) | (((kk >> 3) & 1) << 2)) << 1;
 }
 
-// An operand's loads: one step is 32 loads of 1 KiB, eight per wave, and load i
-// of wave w is KiB 4 i + w of the tile.  Lane l of a load fills the 16 bytes at
+// An operand's loads: one step of a tile of 256 rows (or columns) is 32 loads of
+// 1 KiB, eight per wave, and load i of wave w is KiB 4 i + w of the tile.  Lane l of a load fills the 16 bytes at
 // position l of its KiB, so the swizzle is applied to the address it reads.
 // Rows, columns and (in the last step) contraction positions past the end read
 // the last ones there are, which zero_tail and the epilogue leave out.
-template <Kind K, bool Gated, int ElemBytes>
+template <Kind K, bool Gated, int ElemBytes, int Size>
 struct Loader {
-    // kAcross: loads i + 2, ... are 16 rows below load i, with its swizzle
-    static constexpr int kOffsets = K == kAlong ? 8 : 2;
+    static constexpr int kLoads = Size / 32;
+    // kAcross: tile rows in a KiB; loads i + kOffsets, ... are 16 rows below load i,
+    // with its swizzle
+    static constexpr int kRowsPerKib = 512 / Size, kRowLanes = kWave / kRowsPerKib;
+    static constexpr int kOffsets = K == kAlong ? kLoads : 4 / kRowsPerKib;
     uint32_t voffset[kOffsets];
     const uint8_t* base;          // of the next step
     int64_t step_bytes;
@@ -120,8 +122,8 @@ struct Loader {
             at = at < last ? at : last;
             return (uint32_t)(tile_row<Gated>(o, r) - o.first) * (uint32_t)o.row_bytes + at;
         } else {
-            int kk = kib * 2 + (lane >> 5);
-            const int chunk = (lane & 31) ^ swizzle_across(kk);
+            int kk = kib * kRowsPerKib + lane / kRowLanes;
+            const int chunk = lane % kRowLanes ^ swizzle_across(kk);
             kk = kk < valid ? kk : (int)valid - 1;
             int32_t col = o.first + chunk * 8;
             col = col < o.limit ? col : o.limit - 8;
@@ -177,7 +179,8 @@ __device__ __forceinline__ void stage_elements(const Operand& o, uint8_t* tile, 
                     in = k < len;
                     p = o.base + tile_row<Gated>(o, r) * o.row_bytes + k * 2;
                 } else {
-                    const int kk = piece >> 5, chunk = (piece & 31) ^ swizzle_across(kk);
+                    constexpr int kChunks = Rows / 8;       // of a row
+                    const int kk = piece / kChunks, chunk = piece % kChunks ^ swizzle_across(kk);
                     const int64_t row = step * 64 + kk;
                     const int32_t col = o.first + chunk * 8 + e;
                     in = row < len && col < o.limit;
@@ -200,7 +203,7 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
         const int piece = i * kThreads + threadIdx.x;
         bool past;
         if constexpr (K == kAlong) past = ((piece & 7) ^ ((piece >> 3) & 7)) * 8 >= valid;
-        else past = (piece >> 5) >= valid;
+        else past = piece / (Rows / 8) >= valid;
         if (past) *reinterpret_cast<u32x4*>(tile + piece * 16) = u32x4{0u, 0u, 0u, 0u};
     }
 }
@@ -214,8 +217,9 @@ typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 // .. + 32.  What depends on the lane and not on the block alone is kept in a few
 // LDS addresses (the swizzle's share of a block index is its low three bits);
 // the rest are offsets in the instruction.
-template <Kind K, int Step>
+template <Kind K, int Step, int Size>
 struct Fragments {
+    static constexpr int kRowBytes = Size * 2;          // kAcross: of a tile row
     // blocks whose index differs in its low three bits alone
     static constexpr int kAt = K == kAlong ? 2 : 8 / Step;
     lds_byte* at[kAt];
@@ -232,7 +236,7 @@ struct Fragments {
             const int kk = g * 8 + (j >> 2), sw = swizzle_across(kk) >> 1;
 #pragma unroll
             for (int i = 0; i < kAt; ++i)
-                at[i] = base + kk * 512 + (((first + Step * i) ^ sw) << 5) + (j & 3) * 8;
+                at[i] = base + kk * kRowBytes + (((first + Step * i) ^ sw) << 5) + (j & 3) * 8;
         }
     }
     // The other of the two tiles.
@@ -248,9 +252,9 @@ struct Fragments {
             // elements, and lane i gets column i of them.
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            lds_byte* const p = at[i % kAt] + i / kAt * 8 * 32 + ks * 32 * 512;
+            lds_byte* const p = at[i % kAt] + i / kAt * 8 * 32 + ks * 32 * kRowBytes;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * 512));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * kRowBytes));
             u32x4 r;
             __builtin_memcpy(&r, &lo, 8);
             __builtin_memcpy(reinterpret_cast<char*>(&r) + 8, &hi, 8);
@@ -269,24 +273,30 @@ struct Fragments {
 template <typename T>
 constexpr bool is_fp8() { return __is_same(T, FP8); }
 
-// Tiles of the m and the n operand for one step make a slot of LDS.  Wide: 256
-// rows, two slots, for the matrix cores; narrow: 128 rows and three slots, two
-// steps of loads under way, for experts with so few rows that their weights'
-// bytes are the time, and for FP8, whose float32 sums are made by vector
-// instructions and so have to fit half the registers.
-template <typename T, Mode M, bool Gated, bool Wide>
+// Tiles of the m and the n operand for one step make a slot of LDS.  kWide: 256
+// rows x 256 columns, two slots, for the matrix cores.  kNarrow: 128 rows and
+// three slots, two steps of loads under way, for experts with so few rows that
+// their weights' bytes are the time, and for FP8, whose float32 sums are made by
+// vector instructions and so have to fit half the registers.  kSmall: 128 rows x
+// 128 columns and four slots, for calls with few tiles.
+enum Shape { kWide, kNarrow, kSmall };
+
+template <typename T, Mode M, bool Gated, Shape H>
 struct Tiles {
+    static constexpr bool kIsWide = H == kWide;
     static constexpr Kind kP = M == kWeightGrad ? kAcross : kAlong;   // m side
     static constexpr Kind kQ = M == kForward ? kAlong : kAcross;      // n side
     static constexpr int kElem = is_fp8<T>() ? 1 : 2;
     static constexpr int kStep = kStepBytes / kElem;                  // contraction per step
-    static constexpr int kRows = Wide ? kTileM : kTileM / 2;
-    static constexpr int kSlots = Wide ? 2 : 3;
+    static constexpr int kRows = kIsWide ? kTileM : kTileM / 2;
+    static constexpr int NI = H == kSmall ? 4 : 8;                    // 16-column blocks of a wave
+    static constexpr int kTileN = 2 * NI * 16;
+    static constexpr int kSlots = kIsWide ? 2 : H == kNarrow ? 3 : 4;
     static constexpr int kPBytes = kRows * kStepBytes, kQBytes = kTileN * kStepBytes;
     static constexpr int kScaleBytes = is_fp8<T>() ? 768 : 0;         // 128 rows, 16 blocks
     static constexpr int kSlot = kPBytes + kQBytes + kScaleBytes;
     // Results pass through LDS 16 rows x kStageCols columns of a wave at a time.
-    static constexpr int kStageCols = Wide ? 64 : 32;
+    static constexpr int kStageCols = kIsWide ? 64 : 32;
     static constexpr int kStageRow = kStageCols + 4;  // floats; the rest spreads the banks
     static constexpr int kLds = kSlots * kSlot + kWaves * 16 * kStageRow * 4;
     static constexpr int next(int slot) { return slot + 1 == kSlots ? 0 : slot + 1; }
@@ -303,18 +313,20 @@ struct TileJob {
     const float* q_scales;
 };
 
-template <typename T, Mode M, bool Gated, bool Wide>
+template <typename T, Mode M, bool Gated, Shape H>
 struct Loaders {
-    using S = Tiles<T, M, Gated, Wide>;
-    Loader<S::kP, false, S::kElem> p;
-    Loader<S::kQ, Gated, S::kElem> q;
+    using S = Tiles<T, M, Gated, H>;
+    static constexpr int kNLoads = S::kTileN / 32;
+    Loader<S::kP, false, S::kElem, S::kRows> p;
+    Loader<S::kQ, Gated, S::kElem, S::kTileN> q;
     uint32_t scale_offset;        // fp8: of the lane's row (waves 0, 1) or block (wave 2)
 
     // Loads of the m operand of a tile of 32 MI rows.
     static constexpr int m_loads(int MI) { return S::kP == kAlong ? MI : 8; }
 
     // Readies the loads of a tile and, where its rows are aligned, sets off
-    // those of its first step, and of the second if both are whole.
+    // those of its first step and, as far as there are whole ones, of the steps
+    // after it that have a slot (with two slots the second, else all but one).
     __device__ __forceinline__ void start(const GemmArgs& a, const TileJob& job, uint8_t* lds) {
         if (!a.aligned || job.len <= 0) return;
         p.init(job.p);
@@ -327,10 +339,11 @@ struct Loaders {
                                : (uint32_t)(tile_row<Gated>(job.q, block * 16) >> 7) * row_bytes;
         }
         step(job, lds, 0, 0);
-        if (job.len >= 2 * S::kStep) step(job, lds, 1, 1);
+#pragma unroll
+        for (int s = 1; s < (S::kIsWide ? 2 : S::kSlots - 1); ++s)
+            if (job.len >= (s + 1) * S::kStep) step(job, lds, s, s);
     }
-    // Load i of step s into a slot: first the m operand's, then the eight of
-    // the n operand.
+    // Load i of step s into a slot: first the m operand's, then the n operand's.
     template <bool Whole>
     __device__ __forceinline__ void piece(const TileJob& job, const uint8_t* slot, int64_t s,
                                           int i, int m_loads) {
@@ -360,12 +373,12 @@ struct Loaders {
         if constexpr (is_fp8<T>()) scales(job, slot, s);
         if (whole) {
 #pragma unroll
-            for (int i = 0; i < kM + 8; ++i)
+            for (int i = 0; i < kM + kNLoads; ++i)
                 if (i >= kM || S::kP == kAcross || i * 32 < rows)
                     piece<true>(job, slot, s, i, kM);
         } else {
 #pragma unroll 1
-            for (int i = 0; i < kM + 8; ++i)
+            for (int i = 0; i < kM + kNLoads; ++i)
                 if (i >= kM || S::kP == kAcross || i * 32 < rows)
                     piece<false>(job, slot, s, i, kM);
         }
@@ -380,7 +393,7 @@ struct Loaders {
 // Writes a tile's results.  They pass through LDS, 16 rows x StageCols columns
 // of a wave at a time, so that each row is written in pieces of 64 to 256 bytes.
 // Lane l of a result holds columns 4 (l >> 4) .. + 4 of row l & 15 of a block.
-template <typename OT, Mode M, bool Gated, int StageCols, int MI>
+template <typename OT, Mode M, bool Gated, int StageCols, int MI, int NI>
 __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job,
                                            const f32x4 (&acc)[MI][NI], float* stage, int wm,
                                            int wn) {
@@ -482,10 +495,12 @@ __device__ __forceinline__ void store_tile(const GemmArgs& a, const TileJob& job
 
 // One tile, whose first loads are under way (Loaders::start).  `advance` sets off
 // the next tile's, between the sums and the stores.
-template <typename T, Mode M, bool Gated, bool Wide, int MI, typename F>
+template <typename T, Mode M, bool Gated, Shape H, int MI, typename F>
 __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, uint8_t* lds,
-                                         Loaders<T, M, Gated, Wide>& loads, F&& advance) {
-    using S = Tiles<T, M, Gated, Wide>;
+                                         Loaders<T, M, Gated, H>& loads, F&& advance) {
+    using S = Tiles<T, M, Gated, H>;
+    constexpr int NI = S::NI, kTileN = S::kTileN;
+    constexpr bool Wide = S::kIsWide;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wm = wave & 1, wn = wave >> 1;
     f32x4 acc[MI][NI];
@@ -495,9 +510,10 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
         for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int64_t steps = (job.len + S::kStep - 1) / S::kStep;
     const int64_t whole = job.len / S::kStep;
-    constexpr int kLoads = Loaders<T, M, Gated, Wide>::m_loads(MI) + 8;
-    Fragments<S::kP, 2> fp;
-    Fragments<S::kQ, 1> fq;
+    constexpr int kMLoads = Loaders<T, M, Gated, H>::m_loads(MI);
+    constexpr int kLoads = kMLoads + Loaders<T, M, Gated, H>::kNLoads;
+    Fragments<S::kP, 2, S::kRows> fp;
+    Fragments<S::kQ, 1, kTileN> fq;
     fp.init(lds, wm, is_fp8<T>());
     fq.init(lds + S::kPBytes, wn * NI, is_fp8<T>());
     int at = 0;                                         // the slot of the step at hand
@@ -507,12 +523,22 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
         fq.move(bytes);
         at = S::next(at);
     };
-    // Narrow tiles: loads first .. last of step s + 2.
+    // Other than wide tiles: the loads of the step that comes kSlots - 1 after the
+    // one at hand go into the slot before it, which is free.
+    constexpr int kAhead = S::kSlots - 1;
+    auto free_slot = [&]() { return lds + (at == 0 ? kAhead : at - 1) * S::kSlot; };
     auto load_ahead = [&](int64_t s, int first, int last) {
-        const uint8_t* slot = lds + S::next(S::next(at)) * S::kSlot;
+        const uint8_t* slot = free_slot();
 #pragma unroll
         for (int i = first; i < last; ++i)
-            if (i < kLoads) loads.template piece<true>(job, slot, s + 2, i, kLoads - 8);
+            if (i < kLoads) loads.template piece<true>(job, slot, s + kAhead, i, kMLoads);
+    };
+    // Step s + 1 is there; up to kAhead - 1 whole steps after it are under way.
+    auto wait_for_next = [&](int64_t s) {
+        const int64_t under_way = whole - (s + 2);
+        if (kAhead >= 3 && under_way >= 2) wait_for_all_but<2 * kLoads>();
+        else if (kAhead >= 2 && under_way >= 1) wait_for_all_but<kLoads>();
+        else wait_for_loads();
     };
     if constexpr (is_fp8<T>()) {
         // A step is one scale block.  Each product of 128 positions starts from
@@ -550,14 +576,12 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                     p[(t + 1) & 1] = fp.get_fp8(t + 1);
                     sp[(t + 1) & 1] = row_scale(t + 1);
                     if (more) {
-                        if (t == 0)
-                            loads.scales(job, lds + S::next(S::next(at)) * S::kSlot, s + 2);
+                        if (t == 0) loads.scales(job, free_slot(), s + kAhead);
                         load_ahead(s, t * kPerTurn, (t + 1) * kPerTurn);
                     }
                 }
                 if (kNext && t == kFree) {
-                    if (more) wait_for_all_but<kLoads>();
-                    else wait_for_loads();
+                    wait_for_next(s);
                     __syncthreads();                    // step s + 1 is there, step s is read
                     next_slot();
                     if (more) loads.next();
@@ -591,7 +615,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
 #pragma unroll
         for (int h = 0; h < kScales; ++h) sq[h] = scale(128 + wn * NI + h);
         int64_t s = 0;
-        for (; s + 1 < whole; ++s) multiply(s, std::true_type{}, s + 2 < whole);
+        for (; s + 1 < whole; ++s) multiply(s, std::true_type{}, s + kAhead < whole);
         multiply(s, std::false_type{}, false);
 #pragma unroll
         for (int n = 0; n < 3; ++n) add(n);
@@ -601,8 +625,8 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
         // turns in the last three; so the barrier between two steps stands
         // before these, and the matrix instructions run across it.  The loads
         // of a tile begin when the barrier frees its memory, a few per turn:
-        // with two slots those of step s + 1, most of them in step s, with three
-        // those of step s + 2.
+        // with two slots those of step s + 1, most of them in step s, with more
+        // those of step s + kAhead.
         constexpr int kTurns = 2 * MI, kFree = kTurns - 3;
         constexpr int kPerTurn = Wide ? (2 * kLoads + kTurns - 1) / kTurns
                                       : (kLoads + kFree - 1) / kFree;
@@ -620,7 +644,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                 p[2] = fp.get(2 % MI, 2 / MI);
             }
         };
-        // Next: step s + 1 is whole and follows.  more: step s + 2 is whole.
+        // Next: step s + 1 is whole and follows.  more: the step to load is whole.
         // rest (wide): of the loads of step s + 1, those after the first three
         // turns' are still to be set off.
         auto multiply = [&](int64_t s, auto next, bool rest, bool more) {
@@ -636,8 +660,8 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                 if (!Wide && kNext && t < kFree && more)
                     load_ahead(s, t * kPerTurn, (t + 1) * kPerTurn);
                 if (kNext && t == kFree) {
-                    if (!Wide && more) wait_for_all_but<kLoads>();
-                    else wait_for_loads();
+                    if (Wide) wait_for_loads();
+                    else wait_for_next(s);
                     __syncthreads();                    // step s + 1 is there, step s is read
                     next_slot();
                     if (Wide ? rest : more) loads.next();
@@ -650,7 +674,7 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                     for (int i = turn * kPerTurn; i < (turn + 1) * kPerTurn; ++i)
                         if (i < kLoads)
                             loads.template piece<true>(job, slot, t < kFree ? s + 1 : s + 2, i,
-                                                       kLoads - 8);
+                                                       kMLoads);
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -671,7 +695,8 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
             if (whole == 0) tail(0);
             first_fragments(-1);
             int64_t s = 0;
-            for (; s + 1 < whole; ++s) multiply(s, std::true_type{}, s > 0, s + 2 < whole);
+            for (; s + 1 < whole; ++s)
+                multiply(s, std::true_type{}, s > 0, s + (Wide ? 2 : kAhead) < whole);
             const bool ragged = steps > whole && whole > 0;
             if (ragged) loads.step(job, lds, whole, S::next(at));
             multiply(s, std::false_type{}, false, false);
@@ -698,22 +723,23 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
     advance();
     float* stage = reinterpret_cast<float*>(lds + S::kSlots * S::kSlot) + wave * 16 * S::kStageRow;
     constexpr int kCols = S::kStageCols;
-    if (a.out_dtype == 2) store_tile<BF16, M, Gated, kCols, MI>(a, job, acc, stage, wm, wn);
-    else if (a.out_dtype == 1) store_tile<F16, M, Gated, kCols, MI>(a, job, acc, stage, wm, wn);
-    else store_tile<F32, M, Gated, kCols, MI>(a, job, acc, stage, wm, wn);
+    if (a.out_dtype == 2) store_tile<BF16, M, Gated, kCols>(a, job, acc, stage, wm, wn);
+    else if (a.out_dtype == 1) store_tile<F16, M, Gated, kCols>(a, job, acc, stage, wm, wn);
+    else store_tile<F32, M, Gated, kCols>(a, job, acc, stage, wm, wn);
 }
 
 // Forward and row-gradient products: a persistent grid walks the tiles of all
 // segments, whose number only the device knows.
-template <typename T, Mode M, bool Gated, bool Wide>
+template <typename T, Mode M, bool Gated, Shape H>
 __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
-    using S = Tiles<T, M, Gated, Wide>;
+    using S = Tiles<T, M, Gated, H>;
+    constexpr bool Wide = S::kIsWide;
     __shared__ __align__(16) uint8_t lds[S::kLds];
     __shared__ int32_t first_tile[kMaxExperts + 1];
     __shared__ int32_t wave_total[kWaves];
     auto m_tiles = [](int32_t rows) { return (rows + S::kRows - 1) / S::kRows; };
     count_row_tiles<kThreads>(a, first_tile, wave_total, m_tiles);
-    const int32_t cols_per_tile = Gated ? kTileN / 2 : kTileN;
+    const int32_t cols_per_tile = Gated ? S::kTileN / 2 : S::kTileN;
     const int32_t n_tiles = (int32_t)((a.out_cols + cols_per_tile - 1) / cols_per_tile);
     const int64_t total = (int64_t)uniform(first_tile[a.num_experts]) * n_tiles;
     // Workgroup b runs on XCD b % 8: each XCD takes a contiguous eighth of the tiles.
@@ -753,23 +779,25 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
     };
     int64_t t = begin + blockIdx.x / kXcds;
     if (t >= end) return;
-    Loaders<T, M, Gated, Wide> loads;
+    Loaders<T, M, Gated, H> loads;
     TileJob job = job_of(t);
     loads.start(a, job, lds);
     while (true) {
         const int64_t next = t + gridDim.x / kXcds;
         TileJob next_job;
+        // narrow: looked up ahead, their tiles are short and registers are free
+        if (!Wide && next < end) next_job = job_of(next);
         auto advance = [&]() {
             if (next >= end) return;
-            next_job = job_of(next);
+            if (Wide) next_job = job_of(next);
             loads.start(a, next_job, lds);
         };
-        if (job.m_rows <= 64) run_tile<T, M, Gated, Wide, 2>(a, job, lds, loads, advance);
+        if (job.m_rows <= 64) run_tile<T, M, Gated, H, 2>(a, job, lds, loads, advance);
         else if (!Wide || job.m_rows <= 128)
-            run_tile<T, M, Gated, Wide, 4>(a, job, lds, loads, advance);
+            run_tile<T, M, Gated, H, 4>(a, job, lds, loads, advance);
         else if constexpr (Wide) {
-            if (job.m_rows <= 192) run_tile<T, M, Gated, Wide, 6>(a, job, lds, loads, advance);
-            else run_tile<T, M, Gated, Wide, 8>(a, job, lds, loads, advance);
+            if (job.m_rows <= 192) run_tile<T, M, Gated, H, 6>(a, job, lds, loads, advance);
+            else run_tile<T, M, Gated, H, 8>(a, job, lds, loads, advance);
         }
         if (next >= end) return;
         t = next;
@@ -781,7 +809,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
 // of its expert's segment.
 template <typename T>
 __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs a) {
-    __shared__ __align__(16) uint8_t lds[Tiles<T, kWeightGrad, false, true>::kLds];
+    __shared__ __align__(16) uint8_t lds[Tiles<T, kWeightGrad, false, kWide>::kLds];
+    constexpr int kTileN = Tiles<T, kWeightGrad, false, kWide>::kTileN;
     const int32_t mt = (int32_t)((a.out_rows + kTileM - 1) / kTileM);
     const int32_t nt = (int32_t)((a.out_cols + kTileN - 1) / kTileN);
     const int32_t tiles = mt * nt;
@@ -809,14 +838,14 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs 
         }
         return false;
     };
-    Loaders<T, kWeightGrad, false, true> loads;
+    Loaders<T, kWeightGrad, false, kWide> loads;
     TileJob job;
     if (!find(job)) return;
     loads.start(a, job, lds);
     while (true) {
         TileJob next_job;
         bool more = false;
-        run_tile<T, kWeightGrad, false, true, 8>(a, job, lds, loads, [&]() {
+        run_tile<T, kWeightGrad, false, kWide, 8>(a, job, lds, loads, [&]() {
             t += gridDim.x / kXcds;
             more = find(next_job);
             if (more) loads.start(a, next_job, lds);
@@ -838,6 +867,12 @@ static_assert(MXMOE_GEMM_GROUPS % kXcds == 0, "every XCD has the same number of 
 #define MXMOE_GEMM_NARROW_ROWS 96
 #endif
 constexpr int64_t kNarrowRows = MXMOE_GEMM_NARROW_ROWS;
+// Tiles (of 128 rows x 256 columns, as many as the sizes allow) below which the
+// small ones run.
+#ifndef MXMOE_GEMM_SMALL_TILES
+#define MXMOE_GEMM_SMALL_TILES 512
+#endif
+constexpr int64_t kSmallTiles = MXMOE_GEMM_SMALL_TILES;
 
 template <typename... KArgs>
 hipError_t start(void (*kernel)(KArgs...), const GemmArgs& a, hipStream_t stream) {
@@ -848,22 +883,30 @@ hipError_t start(void (*kernel)(KArgs...), const GemmArgs& a, hipStream_t stream
 }  // namespace
 
 hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t stream) {
-    if (a.dtype == 3)
-        return a.gated ? start(gemm_rows_kernel<FP8, kForward, true, false>, a, stream)
-                       : start(gemm_rows_kernel<FP8, kForward, false, false>, a, stream);
-    const bool wide = a.num_rows > kNarrowRows * a.num_experts;
-    auto go = [&](auto type) {
+    // tiles of 128 rows x 256 columns there can be
+    const int64_t cols = a.gated ? 2 * a.out_cols : a.out_cols;
+    const int64_t row_tiles = a.num_rows / 128 + (a.num_rows < a.num_experts ? a.num_rows
+                                                                             : a.num_experts);
+    const bool small = row_tiles * ((cols + 255) / 256) < kSmallTiles;
+    auto go = [&](auto type, auto mode, auto gated) {
         using T = decltype(type);
-        if (a.transposed)
-            return wide ? start(gemm_rows_kernel<T, kRowGrad, false, true>, a, stream)
-                        : start(gemm_rows_kernel<T, kRowGrad, false, false>, a, stream);
-        if (a.gated)
-            return wide ? start(gemm_rows_kernel<T, kForward, true, true>, a, stream)
-                        : start(gemm_rows_kernel<T, kForward, true, false>, a, stream);
-        return wide ? start(gemm_rows_kernel<T, kForward, false, true>, a, stream)
-                    : start(gemm_rows_kernel<T, kForward, false, false>, a, stream);
+        constexpr Mode M = decltype(mode)::value;
+        constexpr bool G = decltype(gated)::value;
+        if (small) return start(gemm_rows_kernel<T, M, G, kSmall>, a, stream);
+        if constexpr (!is_fp8<T>())
+            if (a.num_rows > kNarrowRows * a.num_experts)
+                return start(gemm_rows_kernel<T, M, G, kWide>, a, stream);
+        return start(gemm_rows_kernel<T, M, G, kNarrow>, a, stream);
     };
-    return a.dtype == 1 ? go(F16{}) : go(BF16{});
+    const std::integral_constant<Mode, kForward> forward;
+    const std::integral_constant<Mode, kRowGrad> row_grad;
+    auto of_type = [&](auto type) {
+        if (a.gated) return go(type, forward, std::true_type{});
+        if constexpr (!is_fp8<decltype(type)>())
+            if (a.transposed) return go(type, row_grad, std::false_type{});
+        return go(type, forward, std::false_type{});
+    };
+    return a.dtype == 3 ? of_type(FP8{}) : a.dtype == 1 ? of_type(F16{}) : of_type(BF16{});
 }
 
 hipError_t launch_grouped_wgrad(const GemmArgs& a, hipStream_t stream) {
