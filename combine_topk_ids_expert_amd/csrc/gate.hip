@@ -32,8 +32,8 @@ __device__ __forceinline__ bool row_in_segment(const int32_t* offsets, const int
 
 __device__ __forceinline__ void silu_mul_grad(float d, float g, float u, float& dg, float& du) {
     const float s = 1.0f / (1.0f + __expf(-g));
-    dg = d * u * s * (1.0f + g * (1.0f - s));
-    du = d * g * s;
+    dg = rounded(d * u * s * (1.0f + g * (1.0f - s)));
+    du = rounded(d * g * s);
 }
 
 // Vec: 8 columns per thread with 16-byte accesses, else one.

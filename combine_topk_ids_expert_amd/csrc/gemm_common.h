@@ -70,8 +70,17 @@ __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b, f32x4 c) {
                                                             0x7f7f7f7f);
 }
 
+// A float32 result that is rounded here and not together with the conversion
+// that follows: the compiler joins a product and its conversion to fp16
+// (v_fma_mixlo_f16) in code for single elements and not in code for vectors, and
+// the two would differ in the last bit.
+__device__ __forceinline__ float rounded(float v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return g / (1.0f + __expf(-g)) * u;
+    return rounded(g / (1.0f + __expf(-g)) * u);
 }
 
 __device__ __forceinline__ void store1(void* out, int dtype, int64_t at, float v) {
@@ -84,29 +93,42 @@ __device__ __forceinline__ void store1(void* out, int dtype, int64_t at, float v
     if (MX_CAN_STORE(p, 2, kSiteGemmOut)) *p = dtype == 2 ? from_f32(BF16{}, v) : from_f32(F16{}, v);
 }
 
+// Whether the bounds of segment e, clipped to the array, are the wrong way round.
+__device__ __forceinline__ bool descends(const GemmArgs& a, int e) {
+    if (!MX_CAN_LOAD(a.offsets + e, 8, kSiteGemmMeta)) return false;
+    const int64_t b = a.offsets[e], t = a.offsets[e + 1];
+    return t < b && t < a.num_rows && b > 0;
+}
+
 // Row tiles before each expert, first[0 .. E], for tiles(count) tiles of an
 // expert with count rows.  For workgroups of `Threads`; `totals` has one
-// element per wave.
+// element per wave.  Ascending offsets make disjoint segments, so that the
+// tiles are fewer than num_rows + E; of others, which may hold every row many
+// times over, no tile is counted.
 template <int Threads, typename F>
 __device__ __forceinline__ void count_row_tiles(const GemmArgs& a, int32_t* first, int32_t* totals,
                                                 F&& tiles) {
     constexpr int kPer = kMaxExperts / Threads;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int c[kPer], sum = 0;
+    bool unordered = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i;
         c[i] = e < a.num_experts ? tiles(segment(a, e).count) : 0;
+        unordered |= e < a.num_experts && descends(a, e);
         sum += c[i];
     }
     const int upto = wave_inclusive_sum(sum);
     if (lane == 63) totals[wave] = upto;
-    __syncthreads();
+    const bool none = __syncthreads_or(unordered);
     int before = upto - sum;
     for (int w = 0; w < wave; ++w) before += totals[w];
+    if (none) before = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i;
+        if (none) c[i] = 0;
         if (e <= a.num_experts) first[e] = before;
         before += c[i];
     }

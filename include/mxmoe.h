@@ -477,8 +477,8 @@ mx_status mx_zero_padding_rows(void* rows, int64_t num_rows, int64_t row_bytes,
  * those without problem_sizes (NULL).  Both are read on the device; offsets
  * are clipped to [0, num_rows] and negative counts are none, so no value of
  * them can make a kernel access memory outside the arrays.  Offsets ascend (as
- * prepare_moe_input writes them); of others, which rows are computed is not
- * defined.  Rows outside the segments (padding, unused capacity) are neither
+ * prepare_moe_input writes them); with others the products leave out as they
+ * are, and which rows the gradients take is not defined.  Rows outside the segments (padding, unused capacity) are neither
  * read nor written: they may hold anything, NaN included, before and after.
  * 1 <= num_experts <= MX_MAX_EXPERTS, num_rows < 2^31, 1 <= n, k <= 2^20.
  * Outputs must not overlap inputs.  Sums are float32; results do not depend on
@@ -530,7 +530,7 @@ mx_status mx_grouped_gemm_fp8(const void* x, const float* x_scales, const void* 
 
 /*
  * grouped_gemm_w4 -- the same with 4-bit weights, for decoding (few rows to an
- * expert; any number works, 64 at a time):
+ * expert; any number works, 16 at a time):
  *
  *   out[r][j] = sum_i x[r][i] * (q[e][j][i] - z) * s,
  *   s = scales[e][j][i / group], z = zeros[e][j][i / group] or 8 (zeros NULL)
