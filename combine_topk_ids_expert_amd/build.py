@@ -39,6 +39,7 @@ ALTGRID_FLAGS = ["-DMXMOE_FUSED_MAX=1024", "-DMXMOE_FUSED_ALWAYS=512", "-DMXMOE_
                  "-DMXMOE_ROW_THREADS=256", "-DMXMOE_COMBINE_THREADS=128",
                  "-DMXMOE_ZERO_THREADS=64", "-DMXMOE_QUANT_THREADS=256",
                  "-DMXMOE_GEMM_GROUPS=64", "-DMXMOE_GEMM_NARROW_ROWS=0", "-DMXMOE_GEMM_SMALL_TILES=0",
+                 "-DMXMOE_WGRAD_SMALL_TILES=0",
                  "-DMXMOE_SKINNY_GROUPS=128"]
 ARCH = "gfx950"
 

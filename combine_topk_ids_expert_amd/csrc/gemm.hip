@@ -157,43 +157,82 @@ struct Loader {
     __device__ __forceinline__ void next() { base += step_bytes; }
 };
 
-// The same for rows that are not 16-byte aligned, element by element, with
-// zeros past every end.
+// The same for rows that are not 16-byte aligned, through registers, with zeros
+// past every end.  A piece of 16 bytes comes by one load from where it lies; one
+// that crosses the end of its row is the row's last 16 bytes, shifted down on the
+// way to LDS.  (Its elements one by one would be a chain of loads in every step
+// of the tiles at the edge: 8 experts, 2000 rows x 2047 transposed 140 us.)
 template <Kind K, bool Gated, int Rows>
-__device__ __forceinline__ void stage_elements(const Operand& o, uint8_t* tile, int64_t step,
-                                               int64_t len) {
-#pragma unroll 1
-    for (int i = 0; i < Rows * kStepBytes / 16 / kThreads; ++i) {
-        const int piece = i * kThreads + threadIdx.x;       // 16 bytes of the tile
-        uint32_t v[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            uint32_t word = 0;
-            for (int h = 0; h < 2; ++h) {
-                const int e = d * 2 + h;
-                const uint8_t* p;
-                bool in;
-                if constexpr (K == kAlong) {
-                    const int r = piece >> 3, chunk = (piece & 7) ^ (r & 7);
-                    const int64_t k = step * 64 + chunk * 8 + e;
-                    in = k < len;
-                    p = o.base + tile_row<Gated>(o, r) * o.row_bytes + k * 2;
-                } else {
-                    constexpr int kChunks = Rows / 8;       // of a row
-                    const int kk = piece / kChunks, chunk = piece % kChunks ^ swizzle_across(kk);
-                    const int64_t row = step * 64 + kk;
-                    const int32_t col = o.first + chunk * 8 + e;
-                    in = row < len && col < o.limit;
-                    p = o.base + row * o.row_bytes + (int64_t)col * 2;
-                }
-                if (in && MX_CAN_LOAD(p, 2, kSiteGemmLoad))
-                    word |= (uint32_t)*reinterpret_cast<const uint16_t*>(p) << (16 * h);
-            }
-            v[d] = word;
-        }
-        *reinterpret_cast<u32x4*>(tile + piece * 16) = u32x4{v[0], v[1], v[2], v[3]};
+struct Pieces {
+    static constexpr int kPieces = Rows * kStepBytes / 16 / kThreads;
+    static constexpr int kChunks = K == kAlong ? 8 : Rows / 8;      // of a tile row
+    u32x4 v[kPieces];
+
+    // Tile row of the thread's piece i, and its first element in the matrix' row.
+    __device__ __forceinline__ static int row(int i) {
+        return (i * kThreads + (int)threadIdx.x) / kChunks;
     }
-}
+    __device__ __forceinline__ static int64_t element(const Operand& o, int64_t step, int i) {
+        const int r = row(i);
+        const int chunk = (int)threadIdx.x % kChunks ^ (K == kAlong ? r & 7 : swizzle_across(r));
+        return (K == kAlong ? step * 64 : (int64_t)o.first) + chunk * 8;
+    }
+    __device__ __forceinline__ static int64_t row_length(const Operand& o, int64_t len) {
+        return K == kAlong ? len : o.limit;
+    }
+    __device__ __forceinline__ void load(const Operand& o, int64_t step, int64_t len) {
+        const int64_t n = row_length(o, len);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint8_t* line;
+            if constexpr (K == kAlong) {
+                line = o.base + tile_row<Gated>(o, row(i)) * o.row_bytes;
+            } else {
+                const int64_t r = step * 64 + row(i);
+                line = o.base + (r < len ? r : len - 1) * o.row_bytes;
+            }
+            const int64_t e = element(o, step, i);
+            v[i] = u32x4{0u, 0u, 0u, 0u};
+            if (n >= 8) {
+                const uint8_t* p = line + (e < n - 8 ? e : n - 8) * 2;
+                if (MX_CAN_LOAD(p, 16, kSiteGemmLoad)) __builtin_memcpy(&v[i], p, 16);
+            } else {
+                // as the last 8 elements of a row, the lower of which do not exist
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+                    const uint16_t* p = reinterpret_cast<const uint16_t*>(line) + j;
+                    if (!MX_CAN_LOAD(p, 2, kSiteGemmLoad)) continue;
+                    const int at = 8 - (int)n + j;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        if (at >> 1 == d) v[i][d] |= (uint32_t)*p << (16 * (at & 1));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const Operand& o, uint8_t* tile, int64_t step,
+                                          int64_t len) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            int64_t here = row_length(o, len) - element(o, step, i);    // elements that exist
+            if (K == kAcross && step * 64 + row(i) >= len) here = 0;
+            uint64_t lo = v[i][0] | (uint64_t)v[i][1] << 32, hi = v[i][2] | (uint64_t)v[i][3] << 32;
+            if (here < 8) {
+                const int bits = here > 0 ? (8 - (int)here) * 16 : 0;
+                if (bits >= 64) {
+                    lo = hi >> (bits - 64);
+                    hi = 0;
+                } else if (bits > 0) {
+                    lo = lo >> bits | hi << (64 - bits);
+                    hi >>= bits;
+                }
+                if (here <= 0) lo = hi = 0;
+            }
+            *reinterpret_cast<u32x4*>(tile + (i * kThreads + threadIdx.x) * 16) =
+                u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        }
+    }
+};
 
 // Zeros at the contraction positions past `valid` (< 64) of a staged tile.
 template <Kind K, int Rows>
@@ -322,7 +361,7 @@ struct Loaders {
     uint32_t scale_offset;        // fp8: of the lane's row (waves 0, 1) or block (wave 2)
 
     // Loads of the m operand of a tile of 32 MI rows.
-    static constexpr int m_loads(int MI) { return S::kP == kAlong ? MI : 8; }
+    static constexpr int m_loads(int MI) { return S::kP == kAlong ? MI : S::kRows / 32; }
 
     // Readies the loads of a tile and, where its rows are aligned, sets off
     // those of its first step and, as far as there are whole ones, of the steps
@@ -708,14 +747,32 @@ __device__ __forceinline__ void run_tile(const GemmArgs& a, const TileJob& job, 
                 first_fragments(-1);
                 multiply(whole, std::false_type{}, false, false);
             }
-        } else {
+        } else if constexpr (!Wide) {
+            // not aligned: the next step is loaded beside this one's products
+            Pieces<S::kP, false, S::kRows> pp;
+            Pieces<S::kQ, Gated, kTileN> pq;
+            auto load = [&](int64_t s) {
+                pp.load(job.p, s, job.len);
+                pq.load(job.q, s, job.len);
+            };
+            auto store = [&](uint8_t* slot, int64_t s) {
+                pp.store(job.p, slot, s, job.len);
+                pq.store(job.q, slot + S::kPBytes, s, job.len);
+                __syncthreads();
+            };
+            if (steps > 0) {
+                load(0);
+                store(lds, 0);
+            }
             for (int64_t s = 0; s < steps; ++s) {
-                __syncthreads();
-                stage_elements<S::kP, false, S::kRows>(job.p, lds, s, job.len);
-                stage_elements<S::kQ, Gated, kTileN>(job.q, lds + S::kPBytes, s, job.len);
-                __syncthreads();
+                const bool more = s + 1 < steps;
+                if (more) load(s + 1);
                 first_fragments(-1);
-                multiply(0, std::false_type{}, false, false);
+                multiply(s, std::false_type{}, false, false);
+                if (more) {
+                    store(lds + S::next(at) * S::kSlot, s + 1);
+                    next_slot();
+                }
             }
         }
     }
@@ -807,13 +864,13 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_rows_kernel(GemmArgs a) {
 
 // Weight gradients: E x (n tiles x k tiles) output tiles, each over the rows
 // of its expert's segment.
-template <typename T>
+template <typename T, Shape H>
 __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs a) {
-    __shared__ __align__(16) uint8_t lds[Tiles<T, kWeightGrad, false, kWide>::kLds];
-    constexpr int kTileN = Tiles<T, kWeightGrad, false, kWide>::kTileN;
-    const int32_t mt = (int32_t)((a.out_rows + kTileM - 1) / kTileM);
-    const int32_t nt = (int32_t)((a.out_cols + kTileN - 1) / kTileN);
-    const int32_t tiles = mt * nt;
+    using S = Tiles<T, kWeightGrad, false, H>;
+    __shared__ __align__(16) uint8_t lds[S::kLds];
+    const int32_t mt = (int32_t)((a.out_rows + S::kRows - 1) / S::kRows);
+    const int32_t nt = (int32_t)((a.out_cols + S::kTileN - 1) / S::kTileN);
+    const int64_t tiles = (int64_t)mt * nt;
     const int xcd = blockIdx.x % kXcds;
     const int64_t per = (tiles + kXcds - 1) / kXcds;    // each XCD: the same tiles of every expert
     const int64_t total = per * a.num_experts;
@@ -826,26 +883,26 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs 
             const Segment sg = uniform_segment(a, e);
             if (at >= tiles || (sg.count == 0 && a.accumulate)) continue;
             const int32_t n_tile = (int32_t)(at / mt), m_tile = (int32_t)(at - (int64_t)n_tile * mt);
-            job.p = Operand{a.x + sg.begin * a.x_row_bytes, a.x_row_bytes, m_tile * kTileM,
+            job.p = Operand{a.x + sg.begin * a.x_row_bytes, a.x_row_bytes, m_tile * S::kRows,
                             (int32_t)a.out_rows, 0};
-            job.q = Operand{a.w + sg.begin * a.w_row_bytes, a.w_row_bytes, n_tile * kTileN,
+            job.q = Operand{a.w + sg.begin * a.w_row_bytes, a.w_row_bytes, n_tile * S::kTileN,
                             (int32_t)a.out_cols, 0};
             job.len = sg.count;
-            job.m_rows = (int32_t)(a.out_rows - (int64_t)m_tile * kTileM < kTileM
-                                       ? a.out_rows - (int64_t)m_tile * kTileM : kTileM);
-            job.out_row0 = (int64_t)e * a.out_rows + (int64_t)m_tile * kTileM;
+            const int64_t rows = a.out_rows - (int64_t)m_tile * S::kRows;
+            job.m_rows = (int32_t)(rows < S::kRows ? rows : S::kRows);
+            job.out_row0 = (int64_t)e * a.out_rows + (int64_t)m_tile * S::kRows;
             return true;
         }
         return false;
     };
-    Loaders<T, kWeightGrad, false, kWide> loads;
+    Loaders<T, kWeightGrad, false, H> loads;
     TileJob job;
     if (!find(job)) return;
     loads.start(a, job, lds);
     while (true) {
         TileJob next_job;
         bool more = false;
-        run_tile<T, kWeightGrad, false, kWide, 8>(a, job, lds, loads, [&]() {
+        run_tile<T, kWeightGrad, false, H, S::kRows / 32>(a, job, lds, loads, [&]() {
             t += gridDim.x / kXcds;
             more = find(next_job);
             if (more) loads.start(a, next_job, lds);
@@ -873,6 +930,11 @@ constexpr int64_t kNarrowRows = MXMOE_GEMM_NARROW_ROWS;
 #define MXMOE_GEMM_SMALL_TILES 512
 #endif
 constexpr int64_t kSmallTiles = MXMOE_GEMM_SMALL_TILES;
+// Weight gradient: tiles of 256 x 256 below which the small ones run.
+#ifndef MXMOE_WGRAD_SMALL_TILES
+#define MXMOE_WGRAD_SMALL_TILES 512
+#endif
+constexpr int64_t kSmallGradTiles = MXMOE_WGRAD_SMALL_TILES;
 
 template <typename... KArgs>
 hipError_t start(void (*kernel)(KArgs...), const GemmArgs& a, hipStream_t stream) {
@@ -894,7 +956,7 @@ hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t stream) {
         constexpr bool G = decltype(gated)::value;
         if (small) return start(gemm_rows_kernel<T, M, G, kSmall>, a, stream);
         if constexpr (!is_fp8<T>())
-            if (a.num_rows > kNarrowRows * a.num_experts)
+            if (a.aligned && a.num_rows > kNarrowRows * a.num_experts)
                 return start(gemm_rows_kernel<T, M, G, kWide>, a, stream);
         return start(gemm_rows_kernel<T, M, G, kNarrow>, a, stream);
     };
@@ -910,8 +972,14 @@ hipError_t launch_grouped_gemm(const GemmArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_grouped_wgrad(const GemmArgs& a, hipStream_t stream) {
-    return a.dtype == 1 ? start(gemm_weight_grad_kernel<F16>, a, stream)
-                        : start(gemm_weight_grad_kernel<BF16>, a, stream);
+    const int64_t tiles = ((a.out_rows + 255) / 256) * ((a.out_cols + 255) / 256) * a.num_experts;
+    auto go = [&](auto type) {
+        using T = decltype(type);
+        return tiles < kSmallGradTiles || !a.aligned
+                   ? start(gemm_weight_grad_kernel<T, kSmall>, a, stream)
+                   : start(gemm_weight_grad_kernel<T, kWide>, a, stream);
+    };
+    return a.dtype == 1 ? go(F16{}) : go(BF16{});
 }
 
 }  // namespace mxmoe
