@@ -4,6 +4,11 @@
 //   s = sigmoid(g);   dg = dh u s (1 + g (1 - s));   du = dh g s
 //
 // gate_up and its gradient hold a row's n gates, then its n ups.
+//
+// Bytes bound it: three 16-bit values read and two written for each h.  A
+// thread takes 8 columns; whether its row is in a segment comes from one ballot
+// over 64 offsets, so padding is not touched.  16384 rows x 2048, bf16: 61 us,
+// 335 MB, 5.5 TB/s.
 #include "device_common.h"
 #include "gemm_common.h"
 #include "launch.h"

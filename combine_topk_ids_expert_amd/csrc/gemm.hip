@@ -10,6 +10,28 @@
 // sizes[e][0] where that is smaller; both are clipped to the arrays, so no
 // value of them makes an access leave the arrays.  Rows outside the segments
 // are neither read nor written.
+//
+// What bounds them.  With many rows to an expert the matrix cores do, with few
+// the bytes of the weights, once each; a weight gradient in float32 writes more
+// than it reads.  A workgroup per CU keeps the sums of one output tile in
+// registers and walks the contraction in steps of 128 bytes per row, which
+// loads put straight into LDS.  It walks the tiles too (persistent): the first
+// step of the next tile is under way while this one is stored.
+//
+// Measured on one MI355X, where a large copy moves 4.9 TB/s, weights alone
+// stream at up to 6.2 TB/s and the library's dense products of 8192^3 and 16384^3
+// reach 1300 and 1560 TFLOP/s in bf16:
+//   32768 rows x 2048 -> 7168, 32 experts, bf16     900 us   1070 TFLOP/s
+//   4096 rows x 7168 -> 2 x 2048 gated, 32 experts  405 us   4.8 TB/s, 590 TFLOP/s
+//   256 rows x 4096 -> 2 x 2048 gated, 256 experts (162 with rows)
+//                                                   950 us   5.7 TB/s
+//   row gradient, 16384 rows x 4096 x 4096, f16     562 us   978 TFLOP/s
+//   weight gradient, the same in bf16 -> float32    743 us   740 TFLOP/s, of which
+//                                                   200 us write 1.07 GB
+//   FP8 16384 rows x 4096 -> 4096, 128 experts      595 us   920 TFLOP/s, 3.9 TB/s
+// Ragged segments cost the large cases their last tiles: 8192^3 with one expert
+// runs at 1310-1370 TFLOP/s.  Tried and slower: the weight gradient's experts
+// turned from XCD to XCD, non-temporal stores, a wait past the stores in flight.
 #include <type_traits>
 
 #include "device_common.h"
@@ -96,8 +118,9 @@ __device__ __forceinline__ int swizzle_across(int kk) {
 }
 
 // An operand's loads: one step of a tile of 256 rows (or columns) is 32 loads of
-// 1 KiB, eight per wave, and load i of wave w is KiB 4 i + w of the tile.  Lane l of a load fills the 16 bytes at
-// position l of its KiB, so the swizzle is applied to the address it reads.
+// 1 KiB, eight per wave, and load i of wave w is KiB 4 i + w of the tile.  Lane l
+// of a load fills the 16 bytes at position l of its KiB, so the swizzle is applied
+// to the address it reads.
 // Rows, columns and (in the last step) contraction positions past the end read
 // the last ones there are, which zero_tail and the epilogue leave out.
 template <Kind K, bool Gated, int ElemBytes, int Size>
@@ -278,7 +301,7 @@ struct Fragments {
                 at[i] = base + kk * kRowBytes + (((first + Step * i) ^ sw) << 5) + (j & 3) * 8;
         }
     }
-    // The other of the two tiles.
+    // On to another slot.
     __device__ __forceinline__ void move(int bytes) {
 #pragma unroll
         for (int i = 0; i < kAt; ++i) at[i] += bytes;
@@ -919,18 +942,25 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_weight_grad_kernel(GemmArgs 
 static_assert(MXMOE_GEMM_GROUPS % kXcds == 0, "every XCD has the same number of workgroups");
 
 // Rows per expert (of the array, the counts are on the device) up to which the
-// narrow tiles run.
+// narrow tiles run.  32 experts, 7168 -> 2 x 2048 gated, narrow against wide:
+// 16 rows each 314 and 356 us, 96 rows 334 and 384, 128 rows 343 and 396, 192
+// rows 537 and 437: they win as long as an expert's rows make one tile, and
+// where the average is 96, ragged counts stay below 128.
 #ifndef MXMOE_GEMM_NARROW_ROWS
 #define MXMOE_GEMM_NARROW_ROWS 96
 #endif
 constexpr int64_t kNarrowRows = MXMOE_GEMM_NARROW_ROWS;
 // Tiles (of 128 rows x 256 columns, as many as the sizes allow) below which the
-// small ones run.
+// small ones run: two for each CU.  1 expert, 2000 rows x 4096 -> 2048: 44 us
+// with them and 91 without; 16 experts, 100 rows x 2704 -> 1304: 36 and 55.  Above,
+// they read more than they spread: FP8 16384 rows 737 us with them, 628 without.
 #ifndef MXMOE_GEMM_SMALL_TILES
 #define MXMOE_GEMM_SMALL_TILES 512
 #endif
 constexpr int64_t kSmallTiles = MXMOE_GEMM_SMALL_TILES;
-// Weight gradient: tiles of 256 x 256 below which the small ones run.
+// Weight gradient: tiles of 256 x 256 below which the small ones run.  1 expert,
+// 2000 rows, 512 x 512: 27 us with them and 63 without; 8 experts, 40 rows, 2048 x
+// 4096 (1024 tiles) 81 and 65; 16 experts, 16384 rows, 4096 x 4096: 1181 and 743.
 #ifndef MXMOE_WGRAD_SMALL_TILES
 #define MXMOE_WGRAD_SMALL_TILES 512
 #endif

@@ -18,6 +18,16 @@
 //   softmax over all:       dl_e = scale p_e ([e chosen] g_e - sum_i p_i g_i)
 //   sigmoid, renormalized:  ds_j = scale (g_j - sum_i w_i g_i) / sum s
 //   sigmoid:                ds_j = scale g_j;   dl = ds s (1 - s)
+//
+// The launch bounds small calls, instructions the large ones.  Up to 12 picks
+// four tokens share a wave, 16 lanes each: the k-th largest of the lanes' maxima
+// bounds the k-th largest key from below, so the keys from there on are a short
+// list, and an expert's place is the number of listed keys before it.  With a
+// wave to a token and one reduction to a pick, 65536 tokens x 288 experts (float32,
+// sigmoid with a bias) took 140 us; this form takes 36: 80 MB, 2.2 TB/s (288
+// sigmoids a token, and keys in 64 bits for those listed).  32 tokens x 256
+// experts: 7 us a call, of which 4 to 5 in the kernel.  Gradient, 16384 tokens x
+// 128 experts, bf16: 5.4 us in the kernel, 9.4 MB.
 #include <type_traits>
 
 #include "device_common.h"
